@@ -75,7 +75,8 @@ typedef enum {
     MLA_ERR_WORKSPACE = 3,     /* workspace missing or smaller than *_workspace_size()    */
     MLA_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed (see error string)    */
     MLA_ERR_DEVICE_BOUNDS = 5, /* device saw an index out of range; the access was skipped */
-    MLA_ERR_TIMEOUT = 6        /* a bounded device-side wait ran out; the kernel returned  */
+    MLA_ERR_TIMEOUT = 6,       /* a bounded device-side wait ran out; the kernel returned  */
+    MLA_ERR_NO_PAGES = 7       /* the page pool had too few free pages; nothing was changed */
 } mla_status;
 
 typedef enum { MLA_BF16 = 0, MLA_FP32 = 1 } mla_dtype;
@@ -164,6 +165,154 @@ MLA_API mla_status mla_decode_absorbed(const mla_dims *dims, const void *q, cons
                                const int32_t *seq_lens_host, int32_t batch, int32_t s_q,
                                int32_t max_pages, int32_t n_pages_total, void *out,
                                void *workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * mla_decode_tree_workspace_size / mla_decode_tree — absorbed attention of a tree of drafted tokens.
+ * Request b's cache holds seq_lens[b] tokens, of which the last n = n_nodes[b] are the nodes of a
+ * tree of drafted tokens (written by mla_cache_append_slots) and the ctx = seq_lens[b] - n before
+ * them its context.  Query j is node j: it sits at position p = ctx + depths[b][j] and attends to
+ * the whole context and to those nodes i < n whose bit i its mask sets:
+ *     s_t = scale * (q_lat . c_t + RoPE(q_rope, p) . k^R_t),  t < ctx, or t = ctx + i with bit i set
+ *     out = W_UV[w] sum_t softmax(s)_t c_t,   q_lat = W_UK[w]^T q_nope
+ * as mla_decode_absorbed otherwise.  The mask is taken as it is: a node that attends to itself sets
+ * its own bit, and nothing asks parents to come before children.  A node that sees nothing (no
+ * context, no bit) gets zeros.
+ *
+ *   q             device [batch, max_nodes, H, d_nope + d_rope]; RoPE part NOT yet rotated.
+ *   page_table    device [batch, max_pages]; only the entries of pages with a token that some node
+ *                 sees are read.
+ *   seq_lens, n_nodes            device [batch];  seq_lens_host, n_nodes_host  host [batch], equal.
+ *                 0 <= n_nodes[b] <= max_nodes <= 64, n_nodes[b] <= seq_lens[b] <= max_pages*page;
+ *                 a request with n_nodes = 0 takes no part.
+ *   depths        device int32 [batch, max_nodes].
+ *   tree_mask     device uint64 [batch, max_nodes], 8-byte aligned; bits >= n are ignored.
+ *   out           device [batch, max_nodes, H, d_v]; node slots j >= n_nodes[b] are not written.
+ *   workspace     as for mla_decode_absorbed, sized by mla_decode_tree_workspace_size.
+ * Cache rows that a node does not see may hold anything, NaN included, and have no part in its result.
+ */
+#define MLA_MAX_TREE_NODES 64
+MLA_API mla_status mla_decode_tree_workspace_size(const mla_dims *dims, int32_t batch, int32_t max_nodes,
+                                                  const int32_t *seq_lens_host, const int32_t *n_nodes_host,
+                                                  size_t *bytes);
+MLA_API mla_status mla_decode_tree(const mla_dims *dims, const void *q, const void *W_uk, const void *W_uv,
+                                   const void *latent_cache, const int32_t *page_table, const int32_t *seq_lens,
+                                   const int32_t *n_nodes, const int32_t *seq_lens_host, const int32_t *n_nodes_host,
+                                   const int32_t *depths, const uint64_t *tree_mask, int32_t batch, int32_t max_nodes,
+                                   int32_t max_pages, int32_t n_pages_total, void *out, void *workspace,
+                                   size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * mla_decode_window_workspace_size / mla_decode_window — mla_decode_absorbed with a sliding window
+ * and a few first tokens that stay visible: query j at position p = seq_lens[b] - s_q + j attends to
+ *     t <= p with t < sinks or t > p - window      (sinks >= 0, window >= 1)
+ * Keys keep the rotation of their own positions.  Only pages with a token that some query of the
+ * request sees are read: the others may have been freed (mla_cache_release), and their page-table
+ * entries may hold anything.  Other arguments, limits and errors as mla_decode_absorbed; s_q <= 4.
+ */
+MLA_API mla_status mla_decode_window_workspace_size(const mla_dims *dims, int32_t batch, int32_t s_q, int32_t sinks,
+                                                    int32_t window, const int32_t *seq_lens_host, size_t *bytes);
+MLA_API mla_status mla_decode_window(const mla_dims *dims, const void *q, const void *W_uk, const void *W_uv,
+                                     const void *latent_cache, const int32_t *page_table, const int32_t *seq_lens,
+                                     const int32_t *seq_lens_host, int32_t batch, int32_t s_q, int32_t sinks,
+                                     int32_t window, int32_t max_pages, int32_t n_pages_total, void *out,
+                                     void *workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * gqla_decode_window_workspace_size / gqla_decode_window — the same window on the GQA path:
+ * gqla_decode_grouped over the tokens that mla_decode_window's queries see.  The queries of a
+ * request share every page read; a cache row that one of them sees has to be finite, since the
+ * others multiply it by a zero probability.  Rows that none sees may hold anything.
+ */
+MLA_API mla_status gqla_decode_window_workspace_size(const mla_dims *dims, int32_t batch, int32_t s_q, int32_t sinks,
+                                                     int32_t window, const int32_t *seq_lens_host, size_t *bytes);
+MLA_API mla_status gqla_decode_window(const mla_dims *dims, const void *q, const void *expanded_cache,
+                                      const void *latent_cache, const int32_t *page_table, const int32_t *seq_lens,
+                                      const int32_t *seq_lens_host, int32_t batch, int32_t s_q, int32_t sinks,
+                                      int32_t window, int32_t max_pages, int32_t n_pages_total, void *out,
+                                      void *workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * mla_cache_append_slots — mla_cache_append with a row's place apart from its position: new token i
+ * becomes row slots[i] of its request (page slots[i] / page_size of the page table), while its RoPE
+ * key turns by positions[i].  The nodes of a drafted tree lie one behind the other in the cache and
+ * sit at ctx + depth; once accepted (mla_cache_accept), a row's place and position agree.
+ *   slots   device [n_tok], 0 <= slot < max_pages*page (else skipped, MLA_ERR_DEVICE_BOUNDS).
+ * gqla_expand_tokens expands such rows when it is given the slots as its positions.
+ */
+MLA_API mla_status mla_cache_append_slots(const mla_dims *dims, const void *h, int32_t hidden, const void *W_dkv,
+                                          const void *W_kr, const int32_t *req_idx, const int32_t *slots,
+                                          const int32_t *positions, int32_t n_tok, const int32_t *page_table,
+                                          int32_t batch, int32_t max_pages, int32_t n_pages_total, void *latent_cache,
+                                          mla_stream_t stream);
+
+/*
+ * Pages of the caches.  A pool of n_pages_total pages is shared by the requests of a batch:
+ *   page_refs    device int32 [n_pages_total], 16-byte aligned: how many page-table entries hold a
+ *                page.  A page is free when it is 0.  Start with zeros.
+ *   page_table   device [batch, max_pages];  seq_lens  device [batch]: request b holds the entries
+ *                [0, ceil(seq_lens[b] / page_size)).  A negative entry is a page that was dropped.
+ *   latent_cache device [n_layers, n_pages_total, page_size, d_c + d_rope], or NULL;
+ *   expanded_cache device [n_layers, n_pages_total, n_groups, page_size, d_nope + d_v], or NULL:
+ *                the caches whose rows a fork or an accepted path moves (one page table for all layers).
+ * Everything is read and changed on the device: the calls need no host copy of a length and can be
+ * captured into a graph.  New pages are the lowest free ids in the order of the requests (forks), so
+ * results do not depend on timing.  Calls on one pool must be ordered (one stream, or events).
+ * Each error below goes to the device error word; n_pages_total <= 2^30, batch and n_fork <= 8192
+ * (release: any batch and n_req).
+ */
+
+/*
+ * mla_cache_reserve — pages for requests that grow: request b gets entries up to
+ * ceil(new_lens[b] / page_size) and seq_lens[b] becomes new_lens[b] (device [batch], not below
+ * seq_lens[b]).  With too few free pages (MLA_ERR_NO_PAGES) or a length that shrinks or passes
+ * max_pages*page (MLA_ERR_DEVICE_BOUNDS) in any request, the call changes nothing.
+ */
+MLA_API mla_status mla_cache_reserve(const mla_dims *dims, const int32_t *new_lens, int32_t *seq_lens,
+                                     int32_t *page_table, int32_t batch, int32_t max_pages, int32_t *page_refs,
+                                     int32_t n_pages_total, mla_stream_t stream);
+
+/*
+ * mla_cache_fork — requests dst_req[i] become copies of what requests src_req[i] were before the call
+ * (device [n_fork] each): full pages are shared (page_refs counts the new holder, dropped entries stay
+ * dropped), the rows of a partly filled last page are copied into a new page, so that source and copy
+ * can both grow.  The destinations must be empty (seq_lens 0), each named once; a source may be named
+ * many times.  A bad index or length or a destination in use (MLA_ERR_DEVICE_BOUNDS) or too few free
+ * pages (MLA_ERR_NO_PAGES) leaves everything as it was.  A page id outside the pool is reported
+ * (MLA_ERR_DEVICE_BOUNDS), and its rows are not copied.
+ */
+MLA_API mla_status mla_cache_fork(const mla_dims *dims, const int32_t *src_req, const int32_t *dst_req, int32_t n_fork,
+                                  int32_t *seq_lens, int32_t *page_table, int32_t batch, int32_t max_pages,
+                                  int32_t *page_refs, int32_t n_pages_total, void *latent_cache, void *expanded_cache,
+                                  int32_t n_layers, mla_stream_t stream);
+
+/*
+ * mla_cache_release — drops pages of requests req_idx[i] (device [n_req]): their entries become -1
+ * and the pages lose a holder.  With first_page and last_page NULL a request drops all its pages and
+ * its length becomes 0; otherwise (device [n_req] each) it drops the entries [first_page[i],
+ * last_page[i]) that it has and keeps its length: the pages behind a sliding window, for instance.
+ * An entry that is named twice is dropped once.  A request or page out of range, or a page that
+ * nobody holds, is reported (MLA_ERR_DEVICE_BOUNDS) and skipped.
+ */
+MLA_API mla_status mla_cache_release(const mla_dims *dims, const int32_t *req_idx, const int32_t *first_page,
+                                     const int32_t *last_page, int32_t n_req, int32_t *seq_lens, int32_t *page_table,
+                                     int32_t batch, int32_t max_pages, int32_t *page_refs, int32_t n_pages_total,
+                                     mla_stream_t stream);
+
+/*
+ * mla_cache_accept — keeps an accepted path of a tree of drafted tokens.  Request b's nodes are the
+ * rows [ctx, ctx + n) with ctx = ctx_lens[b], n = n_nodes[b] <= max_nodes <= 64; its path is the
+ * nodes accepted[b][0..n_accepted[b]), whose indices must rise (device [batch], [batch, max_nodes]).
+ * Their rows move to ctx, ctx + 1, ... in every layer of the caches given, seq_lens[b] becomes
+ * ctx + n_accepted[b], and the pages of the nodes behind it are dropped as by mla_cache_release
+ * (page_refs NULL: they stay).  A request whose counts or indices are not so, or whose rows' pages
+ * are out of range, is left as it was and reported (MLA_ERR_DEVICE_BOUNDS).  The rows written lie
+ * behind the context, in pages that belong to the request alone (mla_cache_fork sees to that).
+ */
+MLA_API mla_status mla_cache_accept(const mla_dims *dims, const int32_t *ctx_lens, const int32_t *n_nodes,
+                                    const int32_t *accepted, const int32_t *n_accepted, int32_t max_nodes,
+                                    int32_t *seq_lens, int32_t *page_table, int32_t batch, int32_t max_pages,
+                                    int32_t *page_refs, int32_t n_pages_total, void *latent_cache,
+                                    void *expanded_cache, int32_t n_layers, mla_stream_t stream);
 
 /*
  * gqla_expand_cache — materialise the GQA path's per-group expanded cache from the latent.

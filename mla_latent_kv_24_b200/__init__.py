@@ -21,20 +21,28 @@ __all__ = [
     "mla_get_device_status", "mla_last_error_string", "mla_version", "mla_set_profile_events",
     "mla_decode_absorbed_noalloc", "NOALLOC_SCRATCH_BYTES", "EXPORTED_SYMBOLS", "mla_select_path",
     "mla_prefill_workspace_size", "mla_prefill_expanded", "gqla_expand_tokens", "mla_debug_decode_fault",
+    "mla_decode_tree_workspace_size", "mla_decode_tree", "mla_decode_window_workspace_size", "mla_decode_window",
+    "gqla_decode_window_workspace_size", "gqla_decode_window", "mla_cache_append_slots", "mla_cache_reserve",
+    "mla_cache_fork", "mla_cache_release", "mla_cache_accept", "MAX_TREE_NODES",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmla.so")
 
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_WORKSPACE",
-          4: "MLA_ERR_CUDA", 5: "MLA_ERR_DEVICE_BOUNDS", 6: "MLA_ERR_TIMEOUT"}
+          4: "MLA_ERR_CUDA", 5: "MLA_ERR_DEVICE_BOUNDS", 6: "MLA_ERR_TIMEOUT", 7: "MLA_ERR_NO_PAGES"}
 MLA_BF16, MLA_FP32 = 0, 1
 
 EXPORTED_SYMBOLS = ["mla_cache_append", "mla_decode_workspace_size", "mla_decode_absorbed",
                     "gqla_expand_cache", "gqla_decode_workspace_size", "gqla_decode_grouped",
                     "mla_get_device_status", "mla_last_error_string", "mla_version", "mla_set_profile_events",
                     "mla_decode_absorbed_noalloc", "mla_select_path", "mla_prefill_workspace_size",
-                    "mla_prefill_expanded", "gqla_expand_tokens", "mla_debug_decode_fault"]
+                    "mla_prefill_expanded", "gqla_expand_tokens", "mla_debug_decode_fault",
+                    "mla_decode_tree_workspace_size", "mla_decode_tree", "mla_decode_window_workspace_size",
+                    "mla_decode_window", "gqla_decode_window_workspace_size", "gqla_decode_window",
+                    "mla_cache_append_slots", "mla_cache_reserve", "mla_cache_fork", "mla_cache_release",
+                    "mla_cache_accept"]
 NOALLOC_SCRATCH_BYTES = 32 << 20
+MAX_TREE_NODES = 64
 
 
 class MlaError(RuntimeError):
@@ -89,6 +97,17 @@ def load() -> ctypes.CDLL:
         "mla_prefill_workspace_size": [D, _I, _I, _P, ctypes.POINTER(_S)],
         "mla_prefill_expanded": [D, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P],
         "mla_debug_decode_fault": [_I, ctypes.c_uint32],
+        "mla_decode_tree_workspace_size": [D, _I, _I, _P, _P, ctypes.POINTER(_S)],
+        "mla_decode_tree": [D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P],
+        "mla_decode_window_workspace_size": [D, _I, _I, _I, _I, _P, ctypes.POINTER(_S)],
+        "mla_decode_window": [D, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _S, _P],
+        "gqla_decode_window_workspace_size": [D, _I, _I, _I, _I, _P, ctypes.POINTER(_S)],
+        "gqla_decode_window": [D, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _S, _P],
+        "mla_cache_append_slots": [D, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P],
+        "mla_cache_reserve": [D, _P, _P, _P, _I, _I, _P, _I, _P],
+        "mla_cache_fork": [D, _P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I, _P],
+        "mla_cache_release": [D, _P, _P, _P, _I, _P, _P, _I, _I, _P, _I, _P],
+        "mla_cache_accept": [D, _P, _P, _P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I, _P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -242,3 +261,175 @@ def mla_debug_decode_fault(withhold_step: int, wait_us: int = 0) -> None:
     of pipeline step `withhold_step` (-1 restores normal operation) and give up every device wait
     after `wait_us` microseconds (0: the 2 s default).  See include/mla.h."""
     _check(load().mla_debug_decode_fault(withhold_step, wait_us))
+
+
+# ---------------------------------------------------------------------------------------
+# Trees, windows and the page pool.  The arrays these calls index by come from several of the
+# caller's structures, so their types, sizes and device are checked here: a short or narrow one
+# would be read past its end.
+# ---------------------------------------------------------------------------------------
+def _arr(name, t, itemsize, n, optional=False) -> Optional[int]:
+    """Device address of a contiguous tensor of at least n elements of `itemsize` bytes on the current device."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is None")
+    p = _dev(t)
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if t.element_size() != itemsize:
+        raise ValueError(f"{name} has {t.element_size()}-byte elements, expected {itemsize}")
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected at least {n}")
+    return p
+
+
+def _host_lens(name, x, n):
+    a, p = _host_i32(x)
+    if a.size < n:
+        raise ValueError(f"{name} has {a.size} elements, expected at least {n}")
+    return a, p
+
+
+def _decode_view_args(dims, q, s_q, cache, n_pages_total, batch, max_pages, page_table, seq_lens, out):
+    e = 4 if dims.dtype == MLA_FP32 else 2
+    rows = batch * s_q * dims.n_heads
+    return e, (_arr("q", q, e, rows * (dims.d_nope + dims.d_rope)),
+               _arr("latent_cache", cache, e, n_pages_total * dims.page_size * (dims.d_c + dims.d_rope)),
+               _arr("page_table", page_table, 4, batch * max_pages), _arr("seq_lens", seq_lens, 4, batch),
+               _arr("out", out, e, rows * dims.d_v))
+
+
+def _weights(dims, e, W_uk, W_uv):
+    g = dims.n_heads // max(1, dims.heads_per_group)
+    return _arr("W_uk", W_uk, e, g * dims.d_nope * dims.d_c), _arr("W_uv", W_uv, e, g * dims.d_v * dims.d_c)
+
+
+def _workspace(ws, nbytes):
+    have = ws.numel() * ws.element_size()
+    return _arr("workspace", ws, ws.element_size(), 0), have if nbytes is None else min(nbytes, have)
+
+
+def mla_decode_tree_workspace_size(dims, batch, max_nodes, seq_lens_host, n_nodes_host) -> int:
+    lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    nodes, np_ = _host_lens("n_nodes_host", n_nodes_host, batch)
+    out = _S(0)
+    _check(load().mla_decode_tree_workspace_size(ctypes.byref(dims), batch, max_nodes, lp, np_, ctypes.byref(out)))
+    return out.value
+
+
+def mla_decode_tree(dims, q, W_uk, W_uv, latent_cache, page_table, seq_lens, n_nodes, seq_lens_host, n_nodes_host,
+                    depths, tree_mask, batch, max_nodes, max_pages, n_pages_total, out, workspace,
+                    workspace_bytes=None, stream=None) -> None:
+    """Attention of a tree of up to 64 drafted tokens per request over the latent cache.  `tree_mask` is an
+    int64 (or uint64) tensor of bit masks; see include/mla.h."""
+    lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    nodes, np_ = _host_lens("n_nodes_host", n_nodes_host, batch)
+    e, (qp, cp, tp, sp, op) = _decode_view_args(dims, q, max_nodes, latent_cache, n_pages_total, batch, max_pages,
+                                                page_table, seq_lens, out)
+    uk, uv = _weights(dims, e, W_uk, W_uv)
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    _check(load().mla_decode_tree(ctypes.byref(dims), qp, uk, uv, cp, tp, sp, _arr("n_nodes", n_nodes, 4, batch), lp,
+                                  np_, _arr("depths", depths, 4, batch * max_nodes),
+                                  _arr("tree_mask", tree_mask, 8, batch * max_nodes), batch, max_nodes, max_pages,
+                                  n_pages_total, op, ws, nbytes, _stream(stream)))
+
+
+def mla_decode_window_workspace_size(dims, batch, s_q, sinks, window, seq_lens_host) -> int:
+    lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    out = _S(0)
+    _check(load().mla_decode_window_workspace_size(ctypes.byref(dims), batch, s_q, sinks, window, lp, ctypes.byref(out)))
+    return out.value
+
+
+def mla_decode_window(dims, q, W_uk, W_uv, latent_cache, page_table, seq_lens, seq_lens_host, batch, s_q, sinks,
+                      window, max_pages, n_pages_total, out, workspace, workspace_bytes=None, stream=None) -> None:
+    lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    e, (qp, cp, tp, sp, op) = _decode_view_args(dims, q, s_q, latent_cache, n_pages_total, batch, max_pages,
+                                                page_table, seq_lens, out)
+    uk, uv = _weights(dims, e, W_uk, W_uv)
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    _check(load().mla_decode_window(ctypes.byref(dims), qp, uk, uv, cp, tp, sp, lp, batch, s_q, sinks, window,
+                                    max_pages, n_pages_total, op, ws, nbytes, _stream(stream)))
+
+
+def gqla_decode_window_workspace_size(dims, batch, s_q, sinks, window, seq_lens_host) -> int:
+    lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    out = _S(0)
+    _check(load().gqla_decode_window_workspace_size(ctypes.byref(dims), batch, s_q, sinks, window, lp,
+                                                    ctypes.byref(out)))
+    return out.value
+
+
+def gqla_decode_window(dims, q, expanded_cache, latent_cache, page_table, seq_lens, seq_lens_host, batch, s_q, sinks,
+                       window, max_pages, n_pages_total, out, workspace, workspace_bytes=None, stream=None) -> None:
+    lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    e, (qp, cp, tp, sp, op) = _decode_view_args(dims, q, s_q, latent_cache, n_pages_total, batch, max_pages,
+                                                page_table, seq_lens, out)
+    g = dims.n_heads // max(1, dims.heads_per_group)
+    ep = _arr("expanded_cache", expanded_cache, e, n_pages_total * g * dims.page_size * (dims.d_nope + dims.d_v))
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    _check(load().gqla_decode_window(ctypes.byref(dims), qp, ep, cp, tp, sp, lp, batch, s_q, sinks, window, max_pages,
+                                     n_pages_total, op, ws, nbytes, _stream(stream)))
+
+
+def mla_cache_append_slots(dims, h, hidden, W_dkv, W_kr, req_idx, slots, positions, n_tok, page_table, batch,
+                           max_pages, n_pages_total, latent_cache, stream=None) -> None:
+    e = 4 if dims.dtype == MLA_FP32 else 2
+    row = dims.d_c + dims.d_rope
+    _check(load().mla_cache_append_slots(
+        ctypes.byref(dims), _arr("h", h, e, n_tok * hidden), hidden, _arr("W_dkv", W_dkv, e, dims.d_c * hidden, True),
+        _arr("W_kr", W_kr, e, dims.d_rope * hidden, True), _arr("req_idx", req_idx, 4, n_tok),
+        _arr("slots", slots, 4, n_tok), _arr("positions", positions, 4, n_tok), n_tok,
+        _arr("page_table", page_table, 4, batch * max_pages), batch, max_pages, n_pages_total,
+        _arr("latent_cache", latent_cache, e, n_pages_total * dims.page_size * row), _stream(stream)))
+
+
+def _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, refs_optional=False):
+    return (_arr("seq_lens", seq_lens, 4, batch), _arr("page_table", page_table, 4, batch * max_pages),
+            _arr("page_refs", page_refs, 4, n_pages_total, refs_optional))
+
+
+def _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total):
+    e = 4 if dims.dtype == MLA_FP32 else 2
+    rows = n_layers * n_pages_total * dims.page_size
+    g = dims.n_heads // max(1, dims.heads_per_group)
+    return (_arr("latent_cache", latent_cache, e, rows * (dims.d_c + dims.d_rope), True),
+            _arr("expanded_cache", expanded_cache, e, rows * g * (dims.d_nope + dims.d_v), True))
+
+
+def mla_cache_reserve(dims, new_lens, seq_lens, page_table, batch, max_pages, page_refs, n_pages_total,
+                      stream=None) -> None:
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total)
+    _check(load().mla_cache_reserve(ctypes.byref(dims), _arr("new_lens", new_lens, 4, batch), s, t, batch, max_pages,
+                                    r, n_pages_total, _stream(stream)))
+
+
+def mla_cache_fork(dims, src_req, dst_req, n_fork, seq_lens, page_table, batch, max_pages, page_refs, n_pages_total,
+                   latent_cache, expanded_cache, n_layers, stream=None) -> None:
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total)
+    lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total)
+    _check(load().mla_cache_fork(ctypes.byref(dims), _arr("src_req", src_req, 4, n_fork),
+                                 _arr("dst_req", dst_req, 4, n_fork), n_fork, s, t, batch, max_pages, r,
+                                 n_pages_total, lat, exp, n_layers, _stream(stream)))
+
+
+def mla_cache_release(dims, req_idx, first_page, last_page, n_req, seq_lens, page_table, batch, max_pages, page_refs,
+                      n_pages_total, stream=None) -> None:
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total)
+    _check(load().mla_cache_release(ctypes.byref(dims), _arr("req_idx", req_idx, 4, n_req),
+                                    _arr("first_page", first_page, 4, n_req, True),
+                                    _arr("last_page", last_page, 4, n_req, True), n_req, s, t, batch, max_pages, r,
+                                    n_pages_total, _stream(stream)))
+
+
+def mla_cache_accept(dims, ctx_lens, n_nodes, accepted, n_accepted, max_nodes, seq_lens, page_table, batch, max_pages,
+                     page_refs, n_pages_total, latent_cache, expanded_cache, n_layers, stream=None) -> None:
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, True)
+    lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total)
+    _check(load().mla_cache_accept(ctypes.byref(dims), _arr("ctx_lens", ctx_lens, 4, batch),
+                                   _arr("n_nodes", n_nodes, 4, batch),
+                                   _arr("accepted", accepted, 4, batch * max_nodes),
+                                   _arr("n_accepted", n_accepted, 4, batch), max_nodes, s, t, batch, max_pages, r,
+                                   n_pages_total, lat, exp, n_layers, _stream(stream)))

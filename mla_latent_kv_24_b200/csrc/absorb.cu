@@ -17,11 +17,18 @@ namespace {
 
 constexpr int RB = 16;
 
+// Position of query j of request b: the s_q queries are the request's last tokens, and a tree's
+// node sits at its depth behind the context.
+__device__ __forceinline__ int query_pos(const View &v, const int *seq_lens, int b, int j, int s_q) {
+    if (v.kind == VIEW_TREE) return seq_lens[b] - v.n_nodes[b] + v.depths[(size_t)b * s_q + j];
+    return seq_lens[b] - s_q + j;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, const T *__restrict__ W_uk,
                                                        const int *__restrict__ seq_lens, int rows, int s_q,
                                                        int H, int hpw, int d_c, int d_r, int d_n, float base,
-                                                       T *__restrict__ q_abs) {
+                                                       T *__restrict__ q_abs, View view) {
     step_begin();
     __shared__ float qn[RB][128];
     const int h = blockIdx.x, w = h / hpw;
@@ -49,7 +56,7 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
     for (int i = threadIdx.x; i < nr * (d_r / 2); i += blockDim.x) {
         const int r = i / (d_r / 2), pi = i % (d_r / 2);
         const int row = row0 + r, b = row / s_q, j = row % s_q;
-        const int p = seq_lens[b] - s_q + j;
+        const int p = query_pos(view, seq_lens, b, j, s_q);
         const T *src = q + ((size_t)row * H + h) * d_qk + d_n + 2 * pi;
         float x0 = to_f32(src[0]), x1 = to_f32(src[1]), cs, sn;
         rope_cos_sin(p, pi, d_r, base, &cs, &sn);
@@ -96,16 +103,16 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, co
 }  // namespace
 
 cudaError_t launch_q_absorb(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch,
-                            int s_q, void *q_abs, cudaStream_t st) {
+                            int s_q, void *q_abs, cudaStream_t st, const View &view) {
     const int rows = batch * s_q;
     dim3 grid(d.H, ceil_div(rows, RB));
     if (d.bf16)
         MLA_STEP_LAUNCH(q_absorb_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, (const __nv_bfloat16 *)q,
                         (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.d_c, d.d_r, d.d_n, d.base,
-                        (__nv_bfloat16 *)q_abs);
+                        (__nv_bfloat16 *)q_abs, view);
     else
         MLA_STEP_LAUNCH(q_absorb_kernel<float>, dim3(grid), dim3(256), 0, st, (const float *)q, (const float *)W_uk,
-                        seq_lens, rows, s_q, d.H, d.hpw, d.d_c, d.d_r, d.d_n, d.base, (float *)q_abs);
+                        seq_lens, rows, s_q, d.H, d.hpw, d.d_c, d.d_r, d.d_n, d.base, (float *)q_abs, view);
     return cudaGetLastError();
 }
 
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *
         for (int i = tid; i < TM * (D_R / 2); i += 256) {
             const int r = i / (D_R / 2), pi = i % (D_R / 2), row = row0 + r;
             if (row >= rows) continue;
-            const int b = row / s_q, j = row % s_q, pos = seq_lens[b] - s_q + j;
+            const int b = row / s_q, j = row % s_q, pos = query_pos(plan.view, seq_lens, b, j, s_q);
             const __nv_bfloat16 *src = q + ((size_t)row * H + h) * D_QK + D_N + 2 * pi;
             float x0 = __bfloat162float(src[0]), x1 = __bfloat162float(src[1]), cs, sn;
             rope_cos_sin(pos, pi, D_R, base, &cs, &sn);

@@ -1,5 +1,6 @@
 // libmla host layer: argument checks, split planning, workspace layout and kernel launches
 // behind the C ABI declared in include/mla.h.
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -132,6 +133,32 @@ mla_status check_batch(const Dims &d, int batch, int s_q, int max_pages, const i
     return MLA_OK;
 }
 
+// A tree call's lengths: seq_lens[b] cached tokens, the last n_nodes[b] of them nodes.
+mla_status check_tree(const Dims &d, int batch, int max_nodes, int max_pages, const int32_t *lens_host,
+                      const int32_t *nodes_host) {
+    if (batch <= 0) return fail(MLA_ERR_INVALID_ARG, "batch must be > 0");
+    if (max_nodes < 1 || max_nodes > MLA_MAX_TREE_NODES)
+        return fail(MLA_ERR_INVALID_ARG, "max_nodes must be 1..%d (got %d)", MLA_MAX_TREE_NODES, max_nodes);
+    if (max_pages <= 0) return fail(MLA_ERR_INVALID_ARG, "max_pages must be > 0");
+    if (!lens_host || !nodes_host) return fail(MLA_ERR_INVALID_ARG, "seq_lens_host / n_nodes_host is NULL");
+    if ((long long)batch * max_nodes > (1 << 20)) return fail(MLA_ERR_UNSUPPORTED, "batch * max_nodes too large");
+    for (int b = 0; b < batch; ++b) {
+        const long long L = lens_host[b];
+        if (nodes_host[b] < 0 || nodes_host[b] > max_nodes)
+            return fail(MLA_ERR_INVALID_ARG, "n_nodes[%d] = %d outside [0, max_nodes=%d]", b, nodes_host[b], max_nodes);
+        if (L < nodes_host[b] || L > (long long)max_pages * d.page)
+            return fail(MLA_ERR_INVALID_ARG, "seq_lens[%d] = %lld outside [n_nodes=%d, max_pages*page=%lld]", b, L,
+                        nodes_host[b], (long long)max_pages * d.page);
+    }
+    return MLA_OK;
+}
+
+mla_status check_window(int sinks, int window) {
+    if (sinks < 0) return fail(MLA_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", sinks);
+    if (window < 1) return fail(MLA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
+    return MLA_OK;
+}
+
 // Workspace layout of one decode call.
 // Plan rows are (request, query) pairs, except on the tensor-core grouped path, where one work
 // item covers all s_q queries of a request (they share every K/V tile), so the plan has one
@@ -144,8 +171,14 @@ struct Layout {
 
 enum Path { ABSORBED = 0, GROUPED = 1 };
 
+// A view and what the host knows of it.  The device pointers inside are NULL while only sizes are asked.
+struct HostView {
+    View v{};
+    const int32_t *n_nodes = nullptr;   // tree: host [batch]
+};
+
 mla_status make_layout(const Dims &d, Path path, bool tc, int sms, int batch, int s_q, const int32_t *lens,
-                       Layout *L) {
+                       Layout *L, const HostView &hv = HostView{}) {
     L->rows = batch * s_q;
     L->tc = tc;
     L->DK = path == ABSORBED ? d.d_c + d.d_r : d.d_n + d.d_r;
@@ -165,8 +198,21 @@ mla_status make_layout(const Dims &d, Path path, bool tc, int sms, int batch, in
     }
     L->plan_sq = (path == GROUPED && grouped_tc_ok(d, s_q)) ? 1 : s_q;
     L->qpi = s_q / L->plan_sq;
-    L->chunk = plan_chunk(lens, batch, L->plan_sq, units, granule);
-    L->n_work = (int)plan_count(lens, batch, L->plan_sq, L->chunk);
+    if (hv.v.kind == VIEW_CAUSAL) {
+        L->chunk = plan_chunk(lens, batch, L->plan_sq, units, granule);
+        L->n_work = (int)plan_count(lens, batch, L->plan_sq, L->chunk);
+    } else {
+        const int psq = L->plan_sq, page = d.page;
+        auto len = [=](int r) {
+            const int b = r / psq;
+            return view_row_len(hv.v.kind, hv.v.sinks, hv.v.window, lens[b], hv.n_nodes ? hv.n_nodes[b] : 0, psq, s_q,
+                                r % psq, page, INT_MAX);
+        };
+        L->chunk = plan_chunk_rows(batch * psq, len, units, granule);
+        const long long n = plan_count_rows(batch * psq, len, L->chunk);
+        if (n > (1 << 24)) return fail(MLA_ERR_UNSUPPORTED, "too many work items (%lld)", n);
+        L->n_work = (int)n;
+    }
     size_t off = 0;
     L->q_off = off;
     off = align256(off + (size_t)L->rows * d.H * L->DK * elt(d));
@@ -243,16 +289,16 @@ mla_status mla_debug_decode_fault(int32_t withhold_step, uint32_t wait_us) {
     return MLA_OK;
 }
 
-mla_status mla_cache_append(const mla_dims *dims, const void *h, int32_t hidden, const void *W_dkv,
-                            const void *W_kr, const int32_t *req_idx, const int32_t *positions, int32_t n_tok,
-                            const int32_t *page_table, int32_t batch, int32_t max_pages, int32_t n_pages_total,
-                            void *latent_cache, mla_stream_t stream) {
+static mla_status run_append(const mla_dims *dims, const void *h, int32_t hidden, const void *W_dkv,
+                             const void *W_kr, const int32_t *req_idx, const int32_t *slots, const int32_t *positions,
+                             int32_t n_tok, const int32_t *page_table, int32_t batch, int32_t max_pages,
+                             int32_t n_pages_total, void *latent_cache, mla_stream_t stream) {
     g_last_error.clear();
     Dims d;
     MLA_TRY(check_dims(dims, &d));
     if (n_tok < 0) return fail(MLA_ERR_INVALID_ARG, "n_tok < 0");
     if (n_tok == 0) return MLA_OK;
-    if (!h || !req_idx || !positions || !page_table || !latent_cache)
+    if (!h || !req_idx || !slots || !positions || !page_table || !latent_cache)
         return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
     if ((W_dkv == nullptr) != (W_kr == nullptr)) return fail(MLA_ERR_INVALID_ARG, "W_dkv and W_kr must both be NULL or both set");
     if (W_dkv == nullptr && hidden != d.d_row())
@@ -262,14 +308,30 @@ mla_status mla_cache_append(const mla_dims *dims, const void *h, int32_t hidden,
     int *err = nullptr;
     MLA_TRY(device_info(&err, nullptr));
     if (append_mma_ok(d, hidden, W_dkv != nullptr) && aligned16(h) && aligned16(W_dkv) && aligned16(W_kr))
-        MLA_CUDA(launch_append_mma(d, h, hidden, W_dkv, W_kr, req_idx, positions, n_tok, page_table, batch, max_pages,
+        MLA_CUDA(launch_append_mma(d, h, hidden, W_dkv, W_kr, req_idx, slots, positions, n_tok, page_table, batch, max_pages,
                                    n_pages_total, latent_cache, err, (cudaStream_t)stream),
                  "launch cache_append (tensor cores)");
     else
-        MLA_CUDA(launch_append(d, h, hidden, W_dkv, W_kr, req_idx, positions, n_tok, page_table, batch, max_pages,
+        MLA_CUDA(launch_append(d, h, hidden, W_dkv, W_kr, req_idx, slots, positions, n_tok, page_table, batch, max_pages,
                                n_pages_total, latent_cache, err, (cudaStream_t)stream),
                  "launch cache_append");
     return MLA_OK;
+}
+
+mla_status mla_cache_append(const mla_dims *dims, const void *h, int32_t hidden, const void *W_dkv,
+                            const void *W_kr, const int32_t *req_idx, const int32_t *positions, int32_t n_tok,
+                            const int32_t *page_table, int32_t batch, int32_t max_pages, int32_t n_pages_total,
+                            void *latent_cache, mla_stream_t stream) {
+    return run_append(dims, h, hidden, W_dkv, W_kr, req_idx, positions, positions, n_tok, page_table, batch, max_pages,
+                      n_pages_total, latent_cache, stream);
+}
+
+mla_status mla_cache_append_slots(const mla_dims *dims, const void *h, int32_t hidden, const void *W_dkv,
+                                  const void *W_kr, const int32_t *req_idx, const int32_t *slots,
+                                  const int32_t *positions, int32_t n_tok, const int32_t *page_table, int32_t batch,
+                                  int32_t max_pages, int32_t n_pages_total, void *latent_cache, mla_stream_t stream) {
+    return run_append(dims, h, hidden, W_dkv, W_kr, req_idx, slots, positions, n_tok, page_table, batch, max_pages,
+                      n_pages_total, latent_cache, stream);
 }
 
 static mla_status decode_workspace(const mla_dims *dims, Path path, int32_t batch, int32_t s_q,
@@ -304,11 +366,19 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                              const void *latent, const void *expanded, const int32_t *page_table,
                              const int32_t *seq_lens, const int32_t *lens_host, int32_t batch, int32_t s_q,
                              int32_t max_pages, int32_t n_pages, void *out, void *ws, size_t ws_bytes,
-                             cudaStream_t st) {
+                             cudaStream_t st, const HostView &hv = HostView{}) {
     g_last_error.clear();
     Dims d;
     MLA_TRY(check_dims(dims, &d));
-    MLA_TRY(check_batch(d, batch, s_q, max_pages, lens_host));
+    if (hv.v.kind == VIEW_TREE)
+        MLA_TRY(check_tree(d, batch, s_q, max_pages, lens_host, hv.n_nodes));
+    else
+        MLA_TRY(check_batch(d, batch, s_q, max_pages, lens_host));
+    if (hv.v.kind == VIEW_WINDOW) MLA_TRY(check_window(hv.v.sinks, hv.v.window));
+    if (hv.v.kind == VIEW_TREE && (!hv.v.n_nodes || !hv.v.depths || !hv.v.mask))
+        return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
+    if (hv.v.kind == VIEW_TREE && ((uintptr_t)hv.v.mask & 7))
+        return fail(MLA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
     if (!q || !latent || !page_table || !seq_lens || !out) return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
     if (path == ABSORBED && (!W_uk || !W_uv)) return fail(MLA_ERR_INVALID_ARG, "W_uk / W_uv is NULL");
     if (path == GROUPED && !expanded) return fail(MLA_ERR_INVALID_ARG, "expanded_cache is NULL");
@@ -322,8 +392,9 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
     MLA_TRY(device_info(&err, &sms));
     const bool tc = path == ABSORBED && use_tc_absorbed(dims);
     Layout L;
-    MLA_TRY(make_layout(d, path, tc, sms, batch, s_q, lens_host, &L));
+    MLA_TRY(make_layout(d, path, tc, sms, batch, s_q, lens_host, &L, hv));
     MLA_TRY(check_ws(L, ws, ws_bytes));
+    if (L.n_work == 0) return MLA_OK;   // a tree call without nodes
     char *w = (char *)ws;
     WorkItem *items = (WorkItem *)(w + L.items_off);
     int *row_first = (int *)(w + L.row_off);
@@ -333,30 +404,33 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
     int *order = tc ? (int *)(w + L.order_off) : nullptr;
     Plan plan{items, row_first, L.n_work, batch * L.plan_sq, L.chunk, order};
 
-    const PlanArgs pa{seq_lens, batch, L.plan_sq, max_pages, d.page, L.chunk, L.n_work, items, row_first, err, order};
+    const PlanArgs pa{seq_lens, batch, L.plan_sq, max_pages, d.page, L.chunk, L.n_work, items, row_first, err, order,
+                      hv.v, s_q};
+    const bool keep_empty = hv.v.kind == VIEW_TREE;   // node slots past a request's count keep their output
     if (path == ABSORBED) {
         if (q_absorb_mma_ok(d)) {
             MLA_CUDA(launch_q_absorb_mma(d, q, W_uk, seq_lens, batch, s_q, qp, pa, st),
                      "launch q_absorb (tensor cores) + plan");
         } else {
             MLA_CUDA(launch_plan(pa, st), "launch plan");
-            MLA_CUDA(launch_q_absorb(d, q, W_uk, seq_lens, batch, s_q, qp, st), "launch q_absorb");
+            MLA_CUDA(launch_q_absorb(d, q, W_uk, seq_lens, batch, s_q, qp, st, hv.v), "launch q_absorb");
         }
         if (tc) {
             ProfileScope prof(st);
             MLA_CUDA(launch_tc_decode(d, qp, latent, page_table, plan, max_pages, n_pages, s_q, part_o, part_ml, err, sms,
-                                      st),
+                                      st, hv.v, seq_lens),
                      "launch tcgen05 decode");
         } else {
             ProfileScope prof(st);
-            SimtDecodeArgs a{qp, latent, nullptr, page_table, plan, max_pages, n_pages, s_q, 0, part_o, part_ml, err};
+            SimtDecodeArgs a{qp, latent, nullptr, page_table, plan, max_pages, n_pages, s_q, 0, part_o, part_ml, err,
+                             hv.v, seq_lens};
             MLA_CUDA(launch_decode_simt(d, a, st), "launch decode (CUDA cores)");
         }
         if (combine_mma_ok(d, L.DV, true)) {
             // The plan's row starts from the host lengths (the device plan is built from the same rule).
             int starts[RowStarts::MAX + 1];
             const int *sp = nullptr;
-            if (L.rows <= RowStarts::MAX && L.plan_sq == s_q) {
+            if (hv.v.kind == VIEW_CAUSAL && L.rows <= RowStarts::MAX && L.plan_sq == s_q) {
                 starts[0] = 0;
                 for (int r = 0; r < L.rows; ++r) {
                     const int b = r / s_q, j = r % s_q;
@@ -364,11 +438,12 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                 }
                 if (starts[L.rows] == L.n_work) sp = starts;
             }
-            MLA_CUDA(launch_combine_mma(d, part_o, part_ml, row_first, sp, L.rows, tc, W_uv, out, st),
+            MLA_CUDA(launch_combine_mma(d, part_o, part_ml, row_first, sp, L.rows, tc, W_uv, out, st, keep_empty),
                      "launch combine + W_UV (tensor cores)");
         }
         else if (!tc)
-            MLA_CUDA(launch_combine(d, part_o, part_ml, row_first, L.rows, 1, L.DV, W_uv, out, st), "launch combine");
+            MLA_CUDA(launch_combine(d, part_o, part_ml, row_first, L.rows, 1, L.DV, W_uv, out, st, keep_empty),
+                     "launch combine");
         else
             return fail(MLA_ERR_UNSUPPORTED, "tcgen05 partials need the tensor-core combine");
     } else {
@@ -376,11 +451,12 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
         if (grouped_tc_ok(d, s_q)) {
             ProfileScope prof(st);
             MLA_CUDA(launch_grouped_decode(d, qp, expanded, latent, seq_lens, page_table, plan, max_pages, n_pages,
-                                           s_q, part_o, part_ml, err, st),
+                                           s_q, part_o, part_ml, err, st, hv.v),
                      "launch grouped decode");
         } else {
             ProfileScope prof(st);
-            SimtDecodeArgs a{qp, latent, expanded, page_table, plan, max_pages, n_pages, s_q, 1, part_o, part_ml, err};
+            SimtDecodeArgs a{qp, latent, expanded, page_table, plan, max_pages, n_pages, s_q, 1, part_o, part_ml, err,
+                             hv.v, seq_lens};
             MLA_CUDA(launch_decode_simt(d, a, st), "launch grouped decode (CUDA cores)");
         }
         MLA_CUDA(launch_combine(d, part_o, part_ml, row_first, L.rows, L.qpi, L.DV, nullptr, out, st), "launch combine");
@@ -451,6 +527,93 @@ mla_status gqla_decode_grouped(const mla_dims *dims, const void *q, const void *
     return run_decode(GROUPED, dims, q, nullptr, nullptr, latent_cache, expanded_cache, page_table, seq_lens,
                       seq_lens_host, batch, s_q, max_pages, n_pages_total, out, workspace, workspace_bytes,
                       (cudaStream_t)stream);
+}
+
+static HostView tree_view(const int32_t *n_nodes, const int32_t *n_nodes_host, const int32_t *depths,
+                          const uint64_t *tree_mask) {
+    HostView hv;
+    hv.v.kind = VIEW_TREE;
+    hv.v.n_nodes = n_nodes;
+    hv.v.depths = depths;
+    hv.v.mask = (const unsigned long long *)tree_mask;
+    hv.n_nodes = n_nodes_host;
+    return hv;
+}
+
+static HostView window_view(int32_t sinks, int32_t window) {
+    HostView hv;
+    hv.v.kind = VIEW_WINDOW;
+    hv.v.sinks = sinks;
+    hv.v.window = window;
+    return hv;
+}
+
+static mla_status view_workspace(const mla_dims *dims, Path path, int32_t batch, int32_t s_q, const int32_t *lens,
+                                 const HostView &hv, size_t *bytes) {
+    g_last_error.clear();
+    Dims d;
+    MLA_TRY(check_dims(dims, &d));
+    if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
+    const int any_pages = INT_MAX / d.page;
+    if (hv.v.kind == VIEW_TREE) {
+        MLA_TRY(check_tree(d, batch, s_q, any_pages, lens, hv.n_nodes));
+    } else {
+        MLA_TRY(check_batch(d, batch, s_q, any_pages, lens));
+        MLA_TRY(check_window(hv.v.sinks, hv.v.window));
+    }
+    int sms = 0;
+    MLA_TRY(device_info(nullptr, &sms));
+    Layout L;
+    MLA_TRY(make_layout(d, path, path == ABSORBED && use_tc_absorbed(dims), sms, batch, s_q, lens, &L, hv));
+    *bytes = L.total;
+    return MLA_OK;
+}
+
+mla_status mla_decode_tree_workspace_size(const mla_dims *dims, int32_t batch, int32_t max_nodes,
+                                          const int32_t *seq_lens_host, const int32_t *n_nodes_host, size_t *bytes) {
+    return view_workspace(dims, ABSORBED, batch, max_nodes, seq_lens_host,
+                          tree_view(nullptr, n_nodes_host, nullptr, nullptr), bytes);
+}
+
+mla_status mla_decode_tree(const mla_dims *dims, const void *q, const void *W_uk, const void *W_uv,
+                           const void *latent_cache, const int32_t *page_table, const int32_t *seq_lens,
+                           const int32_t *n_nodes, const int32_t *seq_lens_host, const int32_t *n_nodes_host,
+                           const int32_t *depths, const uint64_t *tree_mask, int32_t batch, int32_t max_nodes,
+                           int32_t max_pages, int32_t n_pages_total, void *out, void *workspace,
+                           size_t workspace_bytes, mla_stream_t stream) {
+    return run_decode(ABSORBED, dims, q, W_uk, W_uv, latent_cache, nullptr, page_table, seq_lens, seq_lens_host,
+                      batch, max_nodes, max_pages, n_pages_total, out, workspace, workspace_bytes,
+                      (cudaStream_t)stream, tree_view(n_nodes, n_nodes_host, depths, tree_mask));
+}
+
+mla_status mla_decode_window_workspace_size(const mla_dims *dims, int32_t batch, int32_t s_q, int32_t sinks,
+                                            int32_t window, const int32_t *seq_lens_host, size_t *bytes) {
+    return view_workspace(dims, ABSORBED, batch, s_q, seq_lens_host, window_view(sinks, window), bytes);
+}
+
+mla_status mla_decode_window(const mla_dims *dims, const void *q, const void *W_uk, const void *W_uv,
+                             const void *latent_cache, const int32_t *page_table, const int32_t *seq_lens,
+                             const int32_t *seq_lens_host, int32_t batch, int32_t s_q, int32_t sinks, int32_t window,
+                             int32_t max_pages, int32_t n_pages_total, void *out, void *workspace,
+                             size_t workspace_bytes, mla_stream_t stream) {
+    return run_decode(ABSORBED, dims, q, W_uk, W_uv, latent_cache, nullptr, page_table, seq_lens, seq_lens_host,
+                      batch, s_q, max_pages, n_pages_total, out, workspace, workspace_bytes, (cudaStream_t)stream,
+                      window_view(sinks, window));
+}
+
+mla_status gqla_decode_window_workspace_size(const mla_dims *dims, int32_t batch, int32_t s_q, int32_t sinks,
+                                             int32_t window, const int32_t *seq_lens_host, size_t *bytes) {
+    return view_workspace(dims, GROUPED, batch, s_q, seq_lens_host, window_view(sinks, window), bytes);
+}
+
+mla_status gqla_decode_window(const mla_dims *dims, const void *q, const void *expanded_cache,
+                              const void *latent_cache, const int32_t *page_table, const int32_t *seq_lens,
+                              const int32_t *seq_lens_host, int32_t batch, int32_t s_q, int32_t sinks,
+                              int32_t window, int32_t max_pages, int32_t n_pages_total, void *out, void *workspace,
+                              size_t workspace_bytes, mla_stream_t stream) {
+    return run_decode(GROUPED, dims, q, nullptr, nullptr, latent_cache, expanded_cache, page_table, seq_lens,
+                      seq_lens_host, batch, s_q, max_pages, n_pages_total, out, workspace, workspace_bytes,
+                      (cudaStream_t)stream, window_view(sinks, window));
 }
 
 // Prefill layout: q_rot [batch*n_q, H, 192] bf16 | one work item per request | row starts |
@@ -613,6 +776,113 @@ mla_status gqla_expand_tokens(const mla_dims *dims, const void *W_uk, const void
     MLA_CUDA(launch_expand_tokens(d, W_uk, W_uv, latent_cache, req_idx, positions, n_tok, page_table, batch,
                                   max_pages, n_pages_total, expanded_cache, err, (cudaStream_t)stream),
              "launch gqla_expand_tokens");
+    return MLA_OK;
+}
+
+// Arguments every call on the page pool shares.
+static mla_status check_pool(const mla_dims *dims, int32_t *seq_lens, int32_t *page_table, int32_t batch,
+                             int32_t max_pages, int32_t *page_refs, bool need_refs, int32_t n_pages_total, Dims *d,
+                             PagePool *p) {
+    MLA_TRY(check_dims(dims, d));
+    if (!seq_lens || !page_table || (need_refs && !page_refs)) return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
+    if (batch <= 0 || max_pages <= 0 || n_pages_total <= 0)
+        return fail(MLA_ERR_INVALID_ARG, "batch, max_pages, n_pages_total must be > 0");
+    if ((long long)max_pages * d->page > INT_MAX) return fail(MLA_ERR_UNSUPPORTED, "max_pages * page too large");
+    if (n_pages_total > PAGES_MAX_TOTAL) return fail(MLA_ERR_UNSUPPORTED, "n_pages_total too large");
+    if (!aligned16(page_refs)) return fail(MLA_ERR_INVALID_ARG, "page_refs must be 16-byte aligned");
+    *p = PagePool{seq_lens, page_table, page_refs, batch, max_pages, n_pages_total, d->page, nullptr};
+    return MLA_OK;
+}
+
+// The given caches as rows to copy; returns how many.
+static mla_status cache_rows(const Dims &d, void *latent, void *expanded, int32_t n_layers, int32_t n_pages, PageRows *r,
+                             int *n) {
+    *n = 0;
+    if (n_layers < 1) return fail(MLA_ERR_INVALID_ARG, "n_layers must be > 0");
+    if (!aligned16(latent) || !aligned16(expanded))
+        return fail(MLA_ERR_INVALID_ARG, "device tensors must be 16-byte aligned");
+    if ((long long)n_layers * (expanded ? d.n_groups() : 1) > 65535) return fail(MLA_ERR_UNSUPPORTED, "n_layers too large");
+    auto add = [&](void *base, int pieces, size_t row) {
+        const size_t piece = row * d.page, page = piece * pieces;
+        const int vec = row % 16 == 0 ? 16 : row % 4 == 0 ? 4 : 2;
+        r[(*n)++] = PageRows{(char *)base, page * (size_t)n_pages, page, piece, n_layers, pieces, (int)row, vec};
+    };
+    if (latent) add(latent, 1, d.d_row() * elt(d));
+    if (expanded) add(expanded, d.n_groups(), (d.d_n + d.d_v) * elt(d));
+    return MLA_OK;
+}
+
+mla_status mla_cache_reserve(const mla_dims *dims, const int32_t *new_lens, int32_t *seq_lens, int32_t *page_table,
+                             int32_t batch, int32_t max_pages, int32_t *page_refs, int32_t n_pages_total,
+                             mla_stream_t stream) {
+    g_last_error.clear();
+    Dims d;
+    PagePool p;
+    MLA_TRY(check_pool(dims, seq_lens, page_table, batch, max_pages, page_refs, true, n_pages_total, &d, &p));
+    if (!new_lens) return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
+    if (batch > PAGES_MAX_REQS) return fail(MLA_ERR_UNSUPPORTED, "batch must be <= %d", PAGES_MAX_REQS);
+    MLA_TRY(device_info(&p.err, nullptr));
+    MLA_CUDA(launch_cache_reserve(p, new_lens, (cudaStream_t)stream), "launch cache_reserve");
+    return MLA_OK;
+}
+
+mla_status mla_cache_fork(const mla_dims *dims, const int32_t *src_req, const int32_t *dst_req, int32_t n_fork,
+                          int32_t *seq_lens, int32_t *page_table, int32_t batch, int32_t max_pages, int32_t *page_refs,
+                          int32_t n_pages_total, void *latent_cache, void *expanded_cache, int32_t n_layers,
+                          mla_stream_t stream) {
+    g_last_error.clear();
+    Dims d;
+    PagePool p;
+    PageRows rows[2];
+    int n = 0;
+    if (n_fork < 0) return fail(MLA_ERR_INVALID_ARG, "n_fork < 0");
+    MLA_TRY(check_pool(dims, seq_lens, page_table, batch, max_pages, page_refs, true, n_pages_total, &d, &p));
+    MLA_TRY(cache_rows(d, latent_cache, expanded_cache, n_layers, n_pages_total, rows, &n));
+    if (n_fork == 0) return MLA_OK;
+    if (!src_req || !dst_req) return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
+    if (n_fork > PAGES_MAX_REQS) return fail(MLA_ERR_UNSUPPORTED, "n_fork must be <= %d", PAGES_MAX_REQS);
+    MLA_TRY(device_info(&p.err, nullptr));
+    MLA_CUDA(launch_cache_fork(p, src_req, dst_req, n_fork, rows, n, (cudaStream_t)stream), "launch cache_fork");
+    return MLA_OK;
+}
+
+mla_status mla_cache_release(const mla_dims *dims, const int32_t *req_idx, const int32_t *first_page,
+                             const int32_t *last_page, int32_t n_req, int32_t *seq_lens, int32_t *page_table,
+                             int32_t batch, int32_t max_pages, int32_t *page_refs, int32_t n_pages_total,
+                             mla_stream_t stream) {
+    g_last_error.clear();
+    Dims d;
+    PagePool p;
+    if (n_req < 0) return fail(MLA_ERR_INVALID_ARG, "n_req < 0");
+    if ((first_page == nullptr) != (last_page == nullptr))
+        return fail(MLA_ERR_INVALID_ARG, "first_page and last_page must both be NULL or both set");
+    MLA_TRY(check_pool(dims, seq_lens, page_table, batch, max_pages, page_refs, true, n_pages_total, &d, &p));
+    if (n_req == 0) return MLA_OK;
+    if (!req_idx) return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
+    MLA_TRY(device_info(&p.err, nullptr));
+    MLA_CUDA(launch_cache_release(p, req_idx, first_page, last_page, n_req, (cudaStream_t)stream), "launch cache_release");
+    return MLA_OK;
+}
+
+mla_status mla_cache_accept(const mla_dims *dims, const int32_t *ctx_lens, const int32_t *n_nodes,
+                            const int32_t *accepted, const int32_t *n_accepted, int32_t max_nodes, int32_t *seq_lens,
+                            int32_t *page_table, int32_t batch, int32_t max_pages, int32_t *page_refs,
+                            int32_t n_pages_total, void *latent_cache, void *expanded_cache, int32_t n_layers,
+                            mla_stream_t stream) {
+    g_last_error.clear();
+    Dims d;
+    PagePool p;
+    PageRows rows[2];
+    int n = 0;
+    MLA_TRY(check_pool(dims, seq_lens, page_table, batch, max_pages, page_refs, false, n_pages_total, &d, &p));
+    MLA_TRY(cache_rows(d, latent_cache, expanded_cache, n_layers, n_pages_total, rows, &n));
+    if (max_nodes < 1 || max_nodes > MLA_MAX_TREE_NODES)
+        return fail(MLA_ERR_INVALID_ARG, "max_nodes must be 1..%d (got %d)", MLA_MAX_TREE_NODES, max_nodes);
+    if (!ctx_lens || !n_nodes || !accepted || !n_accepted) return fail(MLA_ERR_INVALID_ARG, "NULL device pointer");
+    if (batch > PAGES_MAX_REQS) return fail(MLA_ERR_UNSUPPORTED, "batch must be <= %d", PAGES_MAX_REQS);
+    MLA_TRY(device_info(&p.err, nullptr));
+    MLA_CUDA(launch_cache_accept(p, ctx_lens, n_nodes, accepted, n_accepted, max_nodes, rows, n, (cudaStream_t)stream),
+             "launch cache_accept");
     return MLA_OK;
 }
 

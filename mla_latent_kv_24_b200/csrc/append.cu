@@ -17,7 +17,7 @@ constexpr int TOK = 16, COLS = 64, KT = 32;
 template <typename T>
 __global__ void __launch_bounds__(256) append_kernel(
     const T *__restrict__ h, int hidden, const T *__restrict__ W_dkv, const T *__restrict__ W_kr,
-    const int *__restrict__ req, const int *__restrict__ pos, int n_tok,
+    const int *__restrict__ req, const int *__restrict__ slot, const int *__restrict__ pos, int n_tok,
     const int *__restrict__ page_table, int batch, int max_pages, int n_pages, int page, int d_c,
     int d_r, float base, T *__restrict__ cache, int *err) {
     step_begin();
@@ -64,17 +64,17 @@ __global__ void __launch_bounds__(256) append_kernel(
     }
     if (n >= n_tok) return;
 
-    const int b = req[n], p = pos[n];
-    if (b < 0 || b >= batch || p < 0 || p >= max_pages * page) {
+    const int b = req[n], p = pos[n], t = slot[n];   // row t of the request, RoPE at position p
+    if (b < 0 || b >= batch || t < 0 || t >= max_pages * page) {
         report(err, MLA_ERR_DEVICE_BOUNDS);
         return;
     }
-    const int pid = page_table[(size_t)b * max_pages + p / page];
+    const int pid = page_table[(size_t)b * max_pages + t / page];
     if (pid < 0 || pid >= n_pages) {
         report(err, MLA_ERR_DEVICE_BOUNDS);
         return;
     }
-    T *dst = cache + ((size_t)pid * page + p % page) * d_row;
+    T *dst = cache + ((size_t)pid * page + t % page) * d_row;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int c = c0 + 2 * cp + 32 * half;
@@ -95,17 +95,17 @@ __global__ void __launch_bounds__(256) append_kernel(
 }  // namespace
 
 cudaError_t launch_append(const Dims &d, const void *h, int hidden, const void *W_dkv,
-                          const void *W_kr, const int *req, const int *pos, int n_tok,
+                          const void *W_kr, const int *req, const int *slot, const int *pos, int n_tok,
                           const int *page_table, int batch, int max_pages, int n_pages,
                           void *cache, int *err, cudaStream_t st) {
     dim3 grid(ceil_div(d.d_row(), COLS), ceil_div(n_tok, TOK));
     if (d.bf16)
         MLA_STEP_LAUNCH(append_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, (const __nv_bfloat16 *)h, hidden,
-                        (const __nv_bfloat16 *)W_dkv, (const __nv_bfloat16 *)W_kr, req, pos, n_tok, page_table, batch,
+                        (const __nv_bfloat16 *)W_dkv, (const __nv_bfloat16 *)W_kr, req, slot, pos, n_tok, page_table, batch,
                         max_pages, n_pages, d.page, d.d_c, d.d_r, d.base, (__nv_bfloat16 *)cache, err);
     else
         MLA_STEP_LAUNCH(append_kernel<float>, dim3(grid), dim3(256), 0, st, (const float *)h, hidden,
-                        (const float *)W_dkv, (const float *)W_kr, req, pos, n_tok, page_table, batch, max_pages,
+                        (const float *)W_dkv, (const float *)W_kr, req, slot, pos, n_tok, page_table, batch, max_pages,
                         n_pages, d.page, d.d_c, d.d_r, d.base, (float *)cache, err);
     return cudaGetLastError();
 }
@@ -134,7 +134,7 @@ constexpr int AP_SPLIT = 8, AP_COLS = 32, AP_TOK = 16, AP_TILES = 576 / AP_COLS;
 __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
     append_mma_kernel(const __nv_bfloat16 *__restrict__ h, int hidden, const __nv_bfloat16 *__restrict__ W_dkv,
                       const __nv_bfloat16 *__restrict__ W_kr, const int *__restrict__ req,
-                      const int *__restrict__ pos, int n_tok, const int *__restrict__ page_table, int batch,
+                      const int *__restrict__ slot, const int *__restrict__ pos, int n_tok, const int *__restrict__ page_table, int batch,
                       int max_pages, int n_pages, float base, __nv_bfloat16 *__restrict__ cache, int *err) {
     step_allow_next();   // loads and products touch inputs only; the cache stores wait (below)
     namespace cg = cooperative_groups;
@@ -198,12 +198,12 @@ __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
                     x1 += x.y;
                 }
             }
-            const int b = req[n], p = pos[n];
-            if (b < 0 || b >= batch || p < 0 || p >= max_pages * 64) {
+            const int b = req[n], p = pos[n], t = slot[n];
+            if (b < 0 || b >= batch || t < 0 || t >= max_pages * 64) {
                 report(err, MLA_ERR_DEVICE_BOUNDS);
                 continue;
             }
-            const int pid = page_table[(size_t)b * max_pages + p / 64];
+            const int pid = page_table[(size_t)b * max_pages + t / 64];
             if (pid < 0 || pid >= n_pages) {
                 report(err, MLA_ERR_DEVICE_BOUNDS);
                 continue;
@@ -215,7 +215,7 @@ __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
                 x0 = y0;
                 x1 = y1;
             }
-            __nv_bfloat16 *dst = cache + ((size_t)pid * 64 + p % 64) * D_ROW + col;
+            __nv_bfloat16 *dst = cache + ((size_t)pid * 64 + t % 64) * D_ROW + col;
             *reinterpret_cast<uint32_t *>(dst) = pack_bf16(x0, x1);
         }
     }
@@ -231,16 +231,16 @@ bool append_mma_ok(const Dims &d, int hidden, bool projected) {
 }
 
 cudaError_t launch_append_mma(const Dims &d, const void *h, int hidden, const void *W_dkv, const void *W_kr,
-                              const int *req, const int *pos, int n_tok, const int *page_table, int batch,
-                              int max_pages, int n_pages, void *cache, int *err, cudaStream_t st) {
+                              const int *req, const int *slot, const int *pos, int n_tok, const int *page_table,
+                              int batch, int max_pages, int n_pages, void *cache, int *err, cudaStream_t st) {
     const int ks = hidden / AP_SPLIT, ld = ks + 8;
     const size_t smem = sizeof(__nv_bfloat16) * (size_t)(AP_COLS + AP_TOK) * ld + sizeof(float) * 2 * AP_TOK * AP_COLS;
     cudaError_t e = raise_smem_limit((const void *)append_mma_kernel, smem);
     if (e != cudaSuccess) return e;
     dim3 grid(AP_TILES * AP_SPLIT, ceil_div(n_tok, AP_TOK));
     MLA_STEP_LAUNCH(append_mma_kernel, dim3(grid), dim3(256), smem, st, (const __nv_bfloat16 *)h, hidden,
-                    (const __nv_bfloat16 *)W_dkv, (const __nv_bfloat16 *)W_kr, req, pos, n_tok, page_table, batch,
-                    max_pages, n_pages, d.base, (__nv_bfloat16 *)cache, err);
+                    (const __nv_bfloat16 *)W_dkv, (const __nv_bfloat16 *)W_kr, req, slot, pos, n_tok, page_table,
+                    batch, max_pages, n_pages, d.base, (__nv_bfloat16 *)cache, err);
     return cudaGetLastError();
 }
 

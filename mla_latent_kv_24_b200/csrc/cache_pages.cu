@@ -1,0 +1,459 @@
+// Pages of the caches: reserving, forking, releasing, and moving a tree's accepted rows together.
+//
+// The pool's whole state is page_refs [n_pages]: how many page-table entries name each page.  A page
+// with no entry is free, and allocation takes the lowest free ids in the order of the requests, so
+// neither the pages a call hands out nor the state it leaves depends on the order of atomics, and
+// freeing is a decrement.  The price is that an allocating call reads the counts up to the last page
+// it takes (4 bytes a page: 40,000 pages are 160 KB); one block does it, 16,384 pages at a time.
+//
+// Rows of the caches are copied with 16-byte accesses (2 or 4 bytes where a row's size asks for it).
+// All of it is bound by launches and latency, except forks over many layers, which are bound by the
+// copied bytes.
+#include <algorithm>
+
+#include "kernels.h"
+
+namespace mla {
+namespace {
+
+constexpr int PT = 1024;        // threads of the allocating block
+constexpr int PER = 16;         // counts a thread reads per tile
+constexpr int CAP = PAGES_MAX_REQS;
+
+// Exclusive prefix of v over the block; *total gets the sum.  All PT threads call it.
+__device__ __forceinline__ int block_prefix(int v, int *total) {
+    __shared__ int warp_sum[PT / 32 + 1];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+    }
+    __syncthreads();   // the previous call's readers are done
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const int w = warp_sum[lane];
+        int wi = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, wi, off);
+            if (lane >= off) wi += x;
+        }
+        warp_sum[lane] = wi - w;
+        if (lane == 31) warp_sum[PT / 32] = wi;
+    }
+    __syncthreads();
+    *total = warp_sum[PT / 32];
+    return warp_sum[warp] + incl - v;
+}
+
+// Bit i: page base + i is free, i < PER.
+__device__ __forceinline__ uint32_t free_bits(const int *refs, int n_pages, int base) {
+    uint32_t m = 0;
+    if (base + PER <= n_pages) {
+        const int4 *p = reinterpret_cast<const int4 *>(refs + base);
+        int4 v[PER / 4];
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) v[i] = p[i];
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i)
+            m |= ((uint32_t)(v[i].x == 0) | (uint32_t)(v[i].y == 0) << 1 | (uint32_t)(v[i].z == 0) << 2 |
+                  (uint32_t)(v[i].w == 0) << 3)
+                 << 4 * i;
+    } else {
+        for (int i = 0; base + i < n_pages; ++i) m |= (uint32_t)(refs[base + i] == 0) << i;   // < PER of them
+    }
+    return m;
+}
+
+// Hands the `wanted` lowest free pages to take(rank, page), rank 0 first, and marks them held.
+// False, with nothing changed, if there are fewer.  All PT threads call it.
+template <typename Take>
+__device__ __forceinline__ bool allocate(int *refs, int n_pages, int wanted, const Take &take) {
+    int have = 0;
+    uint32_t first_tile = 0;
+    for (int base = 0; base < n_pages && have < wanted; base += PT * PER) {
+        const int at = base + (int)threadIdx.x * PER;
+        const uint32_t m = at < n_pages ? free_bits(refs, n_pages, at) : 0u;
+        if (base == 0) first_tile = m;
+        int total;
+        block_prefix(__popc(m), &total);
+        have += total;
+    }
+    if (have < wanted) return false;
+    int before = 0;
+    for (int base = 0; before < wanted; base += PT * PER) {
+        const int at = base + (int)threadIdx.x * PER;
+        uint32_t m = base == 0 ? first_tile : at < n_pages ? free_bits(refs, n_pages, at) : 0u;
+        int total;
+        int rank = before + block_prefix(__popc(m), &total);
+        for (; m && rank < wanted; m &= m - 1, ++rank) {
+            const int page = at + __ffs(m) - 1;
+            refs[page] = 1;
+            take(rank, page);
+        }
+        before += total;
+    }
+    return true;
+}
+
+struct Pool {
+    int *seq_lens, *page_table, *refs;
+    int batch, max_pages, n_pages, page;
+    int *err;
+    __device__ __forceinline__ int pages_of(int len) const { return len / page + (len % page != 0); }
+    __device__ __forceinline__ bool fits(int len) const { return len >= 0 && len <= (long long)max_pages * page; }
+    __device__ __forceinline__ int *entry(int b, int k) const { return page_table + (size_t)b * max_pages + k; }
+};
+
+// ------------------------------------------------------------------------------------- reserve
+__global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restrict__ new_lens) {
+    step_begin();
+    __shared__ int off[CAP + 1];
+    const int per = ceil_div(p.batch, PT), b0 = min(p.batch, (int)threadIdx.x * per), b1 = min(p.batch, b0 + per);
+    int mine = 0, bad = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int L = p.seq_lens[b], n = new_lens[b];
+        if (L < 0 || n < L || !p.fits(n)) {
+            bad = 1;
+            off[b] = 0;
+        } else {
+            off[b] = p.pages_of(n) - p.pages_of(L);
+            mine += off[b];
+        }
+    }
+    bad = __syncthreads_or(bad);
+    int total;
+    int at = block_prefix(mine, &total);
+    for (int b = b0; b < b1; ++b) {
+        const int n = off[b];
+        off[b] = at;
+        at += n;
+    }
+    if (threadIdx.x == 0) off[p.batch] = total;
+    __syncthreads();
+    if (bad) {
+        if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const bool ok = allocate(p.refs, p.n_pages, total, [&](int rank, int pg) {
+        int lo = 0, hi = p.batch - 1;   // the last request that starts at or before `rank`
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (off[mid] <= rank) lo = mid;
+            else hi = mid - 1;
+        }
+        *p.entry(lo, p.pages_of(p.seq_lens[lo]) + rank - off[lo]) = pg;
+    });
+    if (!ok) {
+        if (threadIdx.x == 0) report(p.err, MLA_ERR_NO_PAGES);
+        return;
+    }
+    __syncthreads();   // the lengths are read above
+    for (int b = b0; b < b1; ++b) p.seq_lens[b] = new_lens[b];
+}
+
+// ------------------------------------------------------------------------------------- fork
+// Checks and new pages.  Claims the destinations (which must be empty, each named once) by a compare
+// and swap of their length, so that a destination named twice is found whatever the order.  A call
+// that is carried out leaves -1 - length in every destination, which tells the copying blocks so;
+// fork_finish_kernel turns it into the length.
+__global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
+                                                       int n) {
+    step_begin();
+    __shared__ int len[CAP];
+    const int per = ceil_div(n, PT), i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
+    int parts = 0, bad = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int s = src[i], d = dst[i];
+        len[i] = 0;
+        if (s < 0 || s >= p.batch || d < 0 || d >= p.batch) {
+            bad = 1;
+            continue;
+        }
+        len[i] = p.seq_lens[s];
+        if (!p.fits(len[i])) bad = 1;
+        parts += len[i] % p.page > 0;
+    }
+    bad = __syncthreads_or(bad);   // every source is read before any destination is written
+    int n_claimed = 0;
+    if (!bad)
+        for (int i = i0; i < i1; ++i, ++n_claimed)
+            if (atomicCAS(p.seq_lens + dst[i], 0, -1 - i) != 0) {
+                bad = 1;
+                break;
+            }
+    bad = __syncthreads_or(bad);
+    int total;
+    int rank0 = block_prefix(parts, &total);
+    // No destination has pages of its own, so its row holds nothing that is still needed.
+    bool ok = !bad;
+    if (ok) {
+        // The rank-th partial page goes to the rank-th fork with one: each thread's forks are
+        // consecutive, so a rank names a thread's first rank and a count from there.
+        __shared__ int first_rank[PT + 1];
+        first_rank[threadIdx.x] = rank0;
+        if (threadIdx.x == PT - 1) first_rank[PT] = total;
+        __syncthreads();
+        ok = allocate(p.refs, p.n_pages, total, [&](int rank, int pg) {
+            int lo = 0, hi = PT - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (first_rank[mid] <= rank) lo = mid;
+                else hi = mid - 1;
+            }
+            int skip = rank - first_rank[lo], i = min(n, lo * per);
+            for (;; ++i)
+                if (len[i] % p.page > 0 && skip-- == 0) break;
+            *p.entry(dst[i], len[i] / p.page) = pg;
+        });
+    }
+    __syncthreads();
+    for (int i = i0; i < i0 + n_claimed; ++i) p.seq_lens[dst[i]] = ok ? -1 - len[i] : 0;
+    if (!ok && threadIdx.x == 0) report(p.err, bad ? MLA_ERR_DEVICE_BOUNDS : MLA_ERR_NO_PAGES);
+}
+
+// Shares the full pages (block 0 of a fork) and copies the partial page's rows of one piece.
+template <typename V>
+__device__ __forceinline__ void copy_span(char *dst, const char *src, size_t bytes) {
+    const size_t n = bytes / sizeof(V);
+    constexpr int U = 4;
+    const size_t stride = (size_t)blockDim.x;
+    size_t i = threadIdx.x;
+    for (; i + (U - 1) * stride < n; i += U * stride) {
+        V v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = reinterpret_cast<const V *>(src)[i + u * stride];
+#pragma unroll
+        for (int u = 0; u < U; ++u) reinterpret_cast<V *>(dst)[i + u * stride] = v[u];
+    }
+    for (; i < n; i += stride) reinterpret_cast<V *>(dst)[i] = reinterpret_cast<const V *>(src)[i];
+}
+
+constexpr int COPY_BYTES = 16384;   // of a piece per block
+
+template <typename V>
+__global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
+                                                        PageRows rows, int share) {
+    step_begin();
+    const int s = src[blockIdx.x], d = dst[blockIdx.x];
+    if (s < 0 || s >= p.batch || d < 0 || d >= p.batch) return;   // reported by the plan
+    const int L = -1 - p.seq_lens[d];
+    if (L <= 0) return;                                           // refused as a whole, or an empty source
+    const int full = L / p.page, rem = L % p.page;
+    if (share && blockIdx.y == 0 && blockIdx.z == 0)
+        for (int k = threadIdx.x; k < full; k += blockDim.x) {
+            const int pg = *p.entry(s, k);
+            *p.entry(d, k) = pg;
+            if (pg >= p.n_pages) report(p.err, MLA_ERR_DEVICE_BOUNDS);
+            else if (pg >= 0) atomicAdd(p.refs + pg, 1);          // a dropped page (< 0) has no holder to add
+        }
+    if (!rem || !rows.base) return;
+    const int from = *p.entry(s, full), to = *p.entry(d, full);
+    if (from < 0 || from >= p.n_pages) {
+        if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const size_t bytes = (size_t)rem * rows.row_bytes, at = (size_t)blockIdx.z * COPY_BYTES;
+    if (at >= bytes) return;
+    const size_t n = bytes - at < (size_t)COPY_BYTES ? bytes - at : (size_t)COPY_BYTES;
+    copy_span<V>(rows.at(blockIdx.y, to) + at, rows.at(blockIdx.y, from) + at, n);
+}
+
+__global__ void __launch_bounds__(256) fork_finish_kernel(Pool p, const int *__restrict__ dst, int n) {
+    step_begin();
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n || dst[i] < 0 || dst[i] >= p.batch) return;
+    const int x = p.seq_lens[dst[i]];
+    if (x < 0) p.seq_lens[dst[i]] = -1 - x;
+}
+
+// ------------------------------------------------------------------------------------- release
+// Drops a page-table entry: the exchange hands an entry that several threads drop to one of them.
+__device__ __forceinline__ void drop_entry(const Pool &p, int *entry) {
+    const int pg = atomicExch(entry, -1);
+    if (pg < 0) return;   // dropped before
+    if (pg >= p.n_pages) {
+        report(p.err, MLA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    if (atomicSub(p.refs + pg, 1) <= 0) {   // nobody held it
+        atomicAdd(p.refs + pg, 1);
+        report(p.err, MLA_ERR_DEVICE_BOUNDS);
+    }
+}
+
+__global__ void __launch_bounds__(256) release_kernel(Pool p, const int *__restrict__ req, const int *__restrict__ first,
+                                                      const int *__restrict__ last) {
+    step_begin();
+    const int b = req[blockIdx.x];
+    if (b < 0 || b >= p.batch) {
+        if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const int L = p.seq_lens[b];
+    if (!p.fits(L)) {
+        if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    int k0 = 0, k1 = p.pages_of(L);
+    if (first) {
+        k0 = max(0, first[blockIdx.x]);
+        k1 = min(k1, last[blockIdx.x]);
+    }
+    for (int k = k0 + (int)threadIdx.x; k < k1; k += blockDim.x) drop_entry(p, p.entry(b, k));
+    if (!first) {
+        __syncthreads();
+        if (threadIdx.x == 0) p.seq_lens[b] = 0;
+    }
+}
+
+// ------------------------------------------------------------------------------------- accept
+// Whether request b's accepted path is one: node indices that rise and exist, in pages that it has.
+// The same answer in both kernels of a call.  All threads of the block call it.
+__device__ __forceinline__ bool path_ok(const Pool &p, int b, int ctx, int n, const int *acc, int n_acc, int max_nodes) {
+    int bad = 0;
+    if (n < 0 || n > max_nodes || n_acc < 0 || n_acc > n || ctx < 0 || (long long)ctx + n > (long long)p.max_pages * p.page)
+        bad = 1;
+    else
+        for (int k = threadIdx.x; k < n_acc; k += blockDim.x) {
+            if (acc[k] >= n || acc[k] < k || (k && acc[k] <= acc[k - 1])) {   // indices that rise have acc[k] >= k
+                bad = 1;
+                break;
+            }
+            const int from = *p.entry(b, (ctx + acc[k]) / p.page), to = *p.entry(b, (ctx + k) / p.page);
+            if (from < 0 || from >= p.n_pages || to < 0 || to >= p.n_pages) bad = 1;
+        }
+    return !__syncthreads_or(bad);
+}
+
+// Row acc[k] of the nodes moves to row k.  The indices rise, so acc[k] >= k: a thread that takes one
+// column of every row in order never reads a row that it has overwritten, and needs no buffer.
+template <typename V>
+__global__ void __launch_bounds__(128) accept_move_kernel(Pool p, const int *__restrict__ ctx_lens,
+                                                          const int *__restrict__ n_nodes, const int *__restrict__ accepted,
+                                                          const int *__restrict__ n_accepted, int max_nodes,
+                                                          PageRows rows, int units) {
+    step_begin();
+    const int b = blockIdx.y;
+    const int ctx = ctx_lens[b], n = n_nodes[b], n_acc = n_accepted[b];
+    const int *acc = accepted + (size_t)b * max_nodes;
+    if (!path_ok(p, b, ctx, n, acc, n_acc, max_nodes)) return;   // reported by the kernel that follows
+    __shared__ int from_page[MLA_MAX_TREE_NODES], from_row[MLA_MAX_TREE_NODES], to_page[MLA_MAX_TREE_NODES],
+        to_row[MLA_MAX_TREE_NODES], n_move;
+    if (threadIdx.x == 0) n_move = 0;
+    __syncthreads();
+    // Rows that stay are the first ones (acc[k] = k only while every node so far is accepted).
+    if (threadIdx.x < n_acc) {
+        const int k = threadIdx.x, t0 = ctx + acc[k], t1 = ctx + k;
+        from_page[k] = *p.entry(b, t0 / p.page), from_row[k] = t0 % p.page;
+        to_page[k] = *p.entry(b, t1 / p.page), to_row[k] = t1 % p.page;
+        if (acc[k] != k) atomicAdd(&n_move, 1);
+    }
+    __syncthreads();
+    const int cols = rows.row_bytes / (int)sizeof(V);
+    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (id >= (long long)units * cols) return;
+    const int unit = (int)(id / cols), c = (int)(id % cols);
+    constexpr int U = 8;
+    for (int k0 = n_acc - n_move; k0 < n_acc; k0 += U) {
+        V v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k0 + u < n_acc)
+                v[u] = reinterpret_cast<const V *>(rows.at(unit, from_page[k0 + u]) + (size_t)from_row[k0 + u] * rows.row_bytes)[c];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k0 + u < n_acc)
+                reinterpret_cast<V *>(rows.at(unit, to_page[k0 + u]) + (size_t)to_row[k0 + u] * rows.row_bytes)[c] = v[u];
+    }
+}
+
+__global__ void __launch_bounds__(64) accept_trim_kernel(Pool p, const int *__restrict__ ctx_lens,
+                                                         const int *__restrict__ n_nodes, const int *__restrict__ accepted,
+                                                         const int *__restrict__ n_accepted, int max_nodes) {
+    step_begin();
+    const int b = blockIdx.x;
+    const int ctx = ctx_lens[b], n = n_nodes[b], n_acc = n_accepted[b];
+    if (!path_ok(p, b, ctx, n, accepted + (size_t)b * max_nodes, n_acc, max_nodes)) {
+        if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    if (p.refs)
+        for (int k = p.pages_of(ctx + n_acc) + (int)threadIdx.x; k < p.pages_of(ctx + n); k += blockDim.x)
+            drop_entry(p, p.entry(b, k));
+    if (threadIdx.x == 0) p.seq_lens[b] = ctx + n_acc;
+}
+
+Pool pool_of(const PagePool &a) {
+    return Pool{a.seq_lens, a.page_table, a.refs, a.batch, a.max_pages, a.n_pages, a.page, a.err};
+}
+
+template <typename V>
+cudaError_t fork_copy(const Pool &p, const int *src, const int *dst, int n_fork, const PageRows &r, int units, int share,
+                      cudaStream_t st) {
+    const size_t piece = (size_t)p.page * (size_t)r.row_bytes;
+    dim3 grid(n_fork, r.base ? units : 1, r.base ? (unsigned)((piece + COPY_BYTES - 1) / COPY_BYTES) : 1);
+    MLA_STEP_LAUNCH(fork_copy_kernel<V>, grid, dim3(256), 0, st, p, src, dst, r, share);
+    return cudaGetLastError();
+}
+
+template <typename V>
+cudaError_t accept_move(const Pool &p, const int *ctx, const int *n_nodes, const int *accepted, const int *n_accepted,
+                        int max_nodes, const PageRows &r, int units, cudaStream_t st) {
+    const long long threads = (long long)units * (r.row_bytes / (int)sizeof(V));
+    dim3 grid((unsigned)((threads + 127) / 128), p.batch);
+    MLA_STEP_LAUNCH(accept_move_kernel<V>, grid, dim3(128), 0, st, p, ctx, n_nodes, accepted, n_accepted, max_nodes, r,
+                    units);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_reserve(const PagePool &a, const int *new_lens, cudaStream_t st) {
+    MLA_STEP_LAUNCH(reserve_kernel, dim3(1), dim3(PT), 0, st, pool_of(a), new_lens);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_fork(const PagePool &a, const int *src, const int *dst, int n_fork, const PageRows *rows, int n_rows,
+                              cudaStream_t st) {
+    const Pool p = pool_of(a);
+    MLA_STEP_LAUNCH(fork_plan_kernel, dim3(1), dim3(PT), 0, st, p, src, dst, n_fork);
+    cudaError_t e = n_rows ? cudaSuccess : fork_copy<uint4>(p, src, dst, n_fork, PageRows{}, 1, 1, st);
+    for (int i = 0; i < n_rows && e == cudaSuccess; ++i) {
+        const PageRows &r = rows[i];
+        const int units = r.n_layers * r.pieces;
+        e = r.vec == 16  ? fork_copy<uint4>(p, src, dst, n_fork, r, units, i == 0, st)
+            : r.vec == 4 ? fork_copy<uint32_t>(p, src, dst, n_fork, r, units, i == 0, st)
+                         : fork_copy<uint16_t>(p, src, dst, n_fork, r, units, i == 0, st);
+    }
+    if (e != cudaSuccess) return e;
+    MLA_STEP_LAUNCH(fork_finish_kernel, dim3(ceil_div(n_fork, 256)), dim3(256), 0, st, p, dst, n_fork);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_release(const PagePool &a, const int *req, const int *first, const int *last, int n_req,
+                                 cudaStream_t st) {
+    MLA_STEP_LAUNCH(release_kernel, dim3(n_req), dim3(256), 0, st, pool_of(a), req, first, last);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_accept(const PagePool &a, const int *ctx, const int *n_nodes, const int *accepted,
+                                const int *n_accepted, int max_nodes, const PageRows *rows, int n_rows, cudaStream_t st) {
+    const Pool p = pool_of(a);
+    for (int i = 0; i < n_rows; ++i) {
+        const PageRows &r = rows[i];
+        const int units = r.n_layers * r.pieces;
+        const cudaError_t e =
+            r.vec == 16  ? accept_move<uint4>(p, ctx, n_nodes, accepted, n_accepted, max_nodes, r, units, st)
+            : r.vec == 4 ? accept_move<uint32_t>(p, ctx, n_nodes, accepted, n_accepted, max_nodes, r, units, st)
+                         : accept_move<uint16_t>(p, ctx, n_nodes, accepted, n_accepted, max_nodes, r, units, st);
+        if (e != cudaSuccess) return e;
+    }
+    MLA_STEP_LAUNCH(accept_trim_kernel, dim3(p.batch), dim3(64), 0, st, p, ctx, n_nodes, accepted, n_accepted, max_nodes);
+    return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
                                                       const float *__restrict__ part_ml,
                                                       const int *__restrict__ row_first, int rows, int qpi,
                                                       int H, int DV, const T *__restrict__ W_uv, int hpw,
-                                                      int d_v, T *__restrict__ out) {
+                                                      int d_v, T *__restrict__ out, bool keep_empty) {
     step_begin();
     extern __shared__ float O[];  // [RB][DV]
     const int h = blockIdx.x;
@@ -52,10 +52,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
         }
     }
     __syncthreads();
+    auto kept = [&](int r) {   // row row0 + r has no work items and keeps what it holds
+        const int pr = (row0 + r) / qpi;
+        return keep_empty && row_first[pr] == row_first[pr + 1];
+    };
     if (W_uv == nullptr) {
         for (int i = threadIdx.x; i < nr * DV; i += blockDim.x) {
             const int r = i / DV, c = i % DV;
-            out[((size_t)(row0 + r) * H + h) * DV + c] = from_f32<T>(O[r * DV + c]);
+            if (!kept(r)) out[((size_t)(row0 + r) * H + h) * DV + c] = from_f32<T>(O[r * DV + c]);
         }
         return;
     }
@@ -70,7 +74,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
 #pragma unroll
             for (int r = 0; r < RB; ++r) acc[r] += wv * O[r * DV + k];
         }
-        for (int r = 0; r < nr; ++r) out[((size_t)(row0 + r) * H + h) * d_v + v] = from_f32<T>(acc[r]);
+        for (int r = 0; r < nr; ++r)
+            if (!kept(r)) out[((size_t)(row0 + r) * H + h) * d_v + v] = from_f32<T>(acc[r]);
     }
 }
 
@@ -82,7 +87,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) combine_rows_kernel(const float *__restrict__ part_o,
                                                            const float *__restrict__ part_ml,
                                                            const int *__restrict__ row_first, int rows, int qpi,
-                                                           int H, int DV, T *__restrict__ out) {
+                                                           int H, int DV, T *__restrict__ out, bool keep_empty) {
     step_begin();
     const int lane = threadIdx.x % 32;
     const long long wid = (long long)blockIdx.x * 8 + threadIdx.x / 32;
@@ -90,6 +95,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const float *__restri
     const int row = (int)(wid / H), h = (int)(wid % H);
     const int pr = row / qpi, j = row % qpi;
     const int k0 = row_first[pr], k1 = row_first[pr + 1];
+    if (keep_empty && k0 == k1) return;
     auto idx = [&](int k) { return ((size_t)k * qpi + j) * H + h; };
     float M = -INFINITY;
     for (int k = k0 + lane; k < k1; k += 32) M = fmaxf(M, part_ml[idx(k) * 2]);
@@ -138,17 +144,17 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const float *__restri
 }  // namespace
 
 cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part_ml, const int *row_first,
-                           int rows, int qpi, int DV, const void *W_uv, void *out, cudaStream_t st) {
+                           int rows, int qpi, int DV, const void *W_uv, void *out, cudaStream_t st, bool keep_empty) {
     if (W_uv == nullptr && DV % 4 == 0) {
         const long long warps = (long long)rows * d.H;
         if (warps == 0) return cudaSuccess;
         const unsigned blocks = (unsigned)((warps + 7) / 8);
         if (d.bf16)
             MLA_STEP_LAUNCH(combine_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, st, part_o, part_ml,
-                            row_first, rows, qpi, d.H, DV, (__nv_bfloat16 *)out);
+                            row_first, rows, qpi, d.H, DV, (__nv_bfloat16 *)out, keep_empty);
         else
             MLA_STEP_LAUNCH(combine_rows_kernel<float>, dim3(blocks), dim3(256), 0, st, part_o, part_ml, row_first,
-                            rows, qpi, d.H, DV, (float *)out);
+                            rows, qpi, d.H, DV, (float *)out, keep_empty);
         return cudaGetLastError();
     }
     dim3 grid(d.H, ceil_div(rows, RB));
@@ -158,13 +164,13 @@ cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part
         cudaError_t e = raise_smem_limit((const void *)k, smem);
         if (e != cudaSuccess) return e;
         MLA_STEP_LAUNCH(k, dim3(grid), dim3(256), smem, st, part_o, part_ml, row_first, rows, qpi, d.H, DV,
-                        (const __nv_bfloat16 *)W_uv, d.hpw, d.d_v, (__nv_bfloat16 *)out);
+                        (const __nv_bfloat16 *)W_uv, d.hpw, d.d_v, (__nv_bfloat16 *)out, keep_empty);
     } else {
         auto k = combine_kernel<float>;
         cudaError_t e = raise_smem_limit((const void *)k, smem);
         if (e != cudaSuccess) return e;
         MLA_STEP_LAUNCH(k, dim3(grid), dim3(256), smem, st, part_o, part_ml, row_first, rows, qpi, d.H, DV,
-                        (const float *)W_uv, d.hpw, d.d_v, (float *)out);
+                        (const float *)W_uv, d.hpw, d.d_v, (float *)out, keep_empty);
     }
     return cudaGetLastError();
 }
@@ -198,7 +204,8 @@ template <bool OCT>
 __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
     combine_split_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ml,
                          const int *__restrict__ row_first, const RowStarts rs, int rows, int H,
-                         const __nv_bfloat16 *__restrict__ W_uv, int hpw, __nv_bfloat16 *__restrict__ out) {
+                         const __nv_bfloat16 *__restrict__ W_uv, int hpw, __nv_bfloat16 *__restrict__ out,
+                         bool keep_empty) {
     step_allow_next();   // the W_UV slice (an input) streams in while the decode finishes
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
@@ -303,6 +310,7 @@ __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
     // CTA s sums output columns [32 s, 32 s + 32) over the four slices, in slice order.
     for (int i = tid; i < nr * 16; i += 256) {
         const int r = i / 16, v = 32 * s + 2 * (i % 16);
+        if (keep_empty && row_first[row0 + r] == row_first[row0 + r + 1]) continue;
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < XS; ++q) {
@@ -323,7 +331,7 @@ bool combine_mma_ok(const Dims &d, int DV, bool project) {
 
 cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *part_ml, const int *row_first,
                                const int *rows_host, int rows, bool oct_layout, const void *W_uv, void *out,
-                               cudaStream_t st) {
+                               cudaStream_t st, bool keep_empty) {
     RowStarts rs;
     rs.n = 0;
     if (rows_host != nullptr && rows <= RowStarts::MAX) {
@@ -339,7 +347,7 @@ cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *
     cudaError_t e = raise_smem_limit((const void *)k, smem);
     if (e != cudaSuccess) return e;
     MLA_STEP_LAUNCH(k, dim3(grid), dim3(256), smem, st, part_o, part_ml, row_first, rs, rows, d.H,
-                    (const __nv_bfloat16 *)W_uv, d.hpw, (__nv_bfloat16 *)out);
+                    (const __nv_bfloat16 *)W_uv, d.hpw, (__nv_bfloat16 *)out, keep_empty);
     return cudaGetLastError();
 }
 

@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "mla.h"
+#include "view.cuh"
 
 namespace mla {
 
@@ -82,12 +83,14 @@ struct WorkItem {
 // Inputs and outputs of the device-side plan builder (plan_block.cuh).
 struct PlanArgs {
     const int *seq_lens;
-    int batch, s_q, max_pages, page, chunk, n_expected;
+    int batch, s_q, max_pages, page, chunk, n_expected;   // s_q: plan rows per request
     WorkItem *items;     // [n_expected]
     int *row_first;      // [batch * s_q + 1]
     int *err;
     int *order;          // optional: [n_expected] take order of the items (see plan_block), then
                          // [batch * s_q + 1] scratch
+    View view;           // which tokens the rows see (default: causal)
+    int n_q;             // window and tree views: queries per request
 };
 
 struct Plan {

@@ -84,6 +84,7 @@ struct GParams {
     float scale_log2;
     float *part_o, *part_ml;   // [n_work * s_q, H, 128], [n_work * s_q, H, 2]
     int *err;
+    View view;
 };
 
 // Rows of the MMA tiles: CTA = (group g, item), row m = query m / 8 of head g*8 + m % 8; RT row
@@ -92,7 +93,11 @@ struct GParams {
 // Tensor maps (bf16, 128-byte swizzle, 64-column inner blocks):
 //   tm_kv  3-D over the expanded cache [n_pages G 64, 256]: (64, rows, 4), box (64, 64, 4): a page of K_g|V_g
 //   tm_kr  3-D over the latent cache [n_pages 64, 576]: (64, rows, 9), box (64, 64, 1) at block 8: k^R
-template <int RT>
+//
+// With WIN the queries see a sliding window and the sinks (view.cuh).  An item's tokens are then
+// virtual ones of all queries of its request together: a page's rows that no query sees are zeroed
+// like stale ones, and each query masks what the others see of the rest.
+template <int RT, bool WIN>
 __global__ void __launch_bounds__(WARPS * 32, 2)
     grouped_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kr, GParams p) {
     constexpr int ROWS = 16 * RT;
@@ -135,6 +140,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
         }
         return;
     }
+    ItemView iv;
+    if (WIN) iv = item_view(p.view, p.seq_lens, b, -1, p.s_q, PAGE);
     // Queries, already rotated (q_rot = [q_nope | RoPE(q_rope, p_j)], one pass per call): s_q = 2
     // fills the 16 rows of one tile, s_q = 1 the first 8; rows past the last query are zero.
     for (int i = tid; i < ROWS * (D_QK / 8); i += blockDim.x) {   // 16-byte chunks
@@ -150,7 +157,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     // (a row coordinate past the end).  Rows past the chunk's end on its ragged last page hold
     // whatever the slots hold, NaN included; each warp zeroes its own rows of them before use.
     auto issue_page = [&](int i) {
-        int pid = p.page_table[(size_t)b * p.max_pages + it.t0 / PAGE + i];
+        const int v0 = it.t0 + PAGE * i;
+        int pid = p.page_table[(size_t)b * p.max_pages + (WIN ? iv.token(v0) : v0) / PAGE];
         if (pid < 0 || pid >= p.n_pages) {
             report(p.err, MLA_ERR_DEVICE_BOUNDS);
             pid = p.n_pages;
@@ -203,7 +211,19 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
         if (!ok) break;
         const uint8_t *tkv = gsm + STAGE * st, *tkr = tkv + KV_BYTES;
         const int valid = it.t1 - (it.t0 + PAGE * i);
-        if (valid < 16 * warp + 16) {   // this warp's rows past the chunk's end: zero them
+        const int page_t0 = WIN ? iv.token(it.t0 + PAGE * i) : it.t0 + PAGE * i;   // the page's first token
+        if constexpr (WIN) {   // this warp's rows that no query sees: zero them
+            const uint32_t rows = (uint32_t)(iv.seen64(page_t0) >> (16 * warp)) & 0xffffu;
+            if (rows != 0xffffu) {
+                for (int e = lane; e < 16 * 5 * 8; e += 32) {
+                    const int rr = e / 40, r = 16 * warp + rr, q = e % 40;
+                    if ((rows >> rr) & 1u) continue;
+                    uint8_t *d = const_cast<uint8_t *>(q < 32 ? tkv + (q / 8) * BLK : tkr) + r * 128 + 16 * (q % 8);
+                    *reinterpret_cast<uint4 *>(d) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+        } else if (valid < 16 * warp + 16) {   // this warp's rows past the chunk's end: zero them
             for (int e = lane; e < 16 * 5 * 8; e += 32) {
                 const int r = 16 * warp + e / 40, q = e % 40;   // 40 chunks of 16 B per row (4 KV blocks + k^R)
                 if (r < valid) continue;
@@ -246,7 +266,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
             }
         }
         // Mask, scale, online softmax per row (rows gid and gid + 8 of each tile; 4 tokens per row here).
-        const int tok_base = it.t0 + PAGE * i + 16 * warp;
+        const int tok_base = page_t0 + 16 * warp;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -255,9 +275,14 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int tk = tok_base + 8 * nt + 2 * t4 + e;
-                    const bool in = tk < it.t1;
-                    s[t][nt][e] = (in && tk <= lim[t][0]) ? s[t][nt][e] * p.scale_log2 : -INFINITY;
-                    s[t][nt][2 + e] = (in && tk <= lim[t][1]) ? s[t][nt][2 + e] * p.scale_log2 : -INFINITY;
+                    // Causal: inside the chunk and not past the query.  Window: not past the query, and in
+                    // its window (or a sink); a chunk that is not the row's last ends between pages.
+                    auto sees = [&](int limit) {
+                        if (WIN) return tk <= limit && (tk < p.view.sinks || tk > limit - p.view.window);
+                        return tk < it.t1 && tk <= limit;
+                    };
+                    s[t][nt][e] = sees(lim[t][0]) ? s[t][nt][e] * p.scale_log2 : -INFINITY;
+                    s[t][nt][2 + e] = sees(lim[t][1]) ? s[t][nt][2 + e] * p.scale_log2 : -INFINITY;
                     mx0 = fmaxf(mx0, s[t][nt][e]);
                     mx1 = fmaxf(mx1, s[t][nt][2 + e]);
                 }
@@ -475,22 +500,22 @@ static bool grouped_maps(const void *expanded, const void *latent, int n_pages, 
 
 cudaError_t launch_grouped_decode(const Dims &d, const void *q, const void *expanded, const void *latent,
                                   const int *seq_lens, const int *page_table, const Plan &plan, int max_pages,
-                                  int n_pages, int s_q, float *part_o, float *part_ml, int *err, cudaStream_t st) {
+                                  int n_pages, int s_q, float *part_o, float *part_ml, int *err, cudaStream_t st,
+                                  const View &view) {
     if (plan.n_work == 0) return cudaSuccess;
-    const GParams p = grouped_params(d, q, expanded, latent, seq_lens, page_table, plan, max_pages, n_pages, s_q,
+    GParams p = grouped_params(d, q, expanded, latent, seq_lens, page_table, plan, max_pages, n_pages, s_q,
                                      part_o, part_ml, err);
+    p.view = view;
     CUtensorMap tm_kv, tm_kr;
     if (!grouped_maps(expanded, latent, n_pages, d.H / GH, &tm_kv, &tm_kr)) return cudaErrorInvalidValue;
     dim3 grid(d.H / GH, std::min(plan.n_work, 65535), ceil_div(plan.n_work, 65535));
-    if (s_q <= 2) {
-        cudaError_t e = raise_smem_limit((const void *)grouped_decode_kernel<1>, smem_bytes(1));
-        if (e != cudaSuccess) return e;
-        MLA_STEP_LAUNCH(grouped_decode_kernel<1>, dim3(grid), dim3(WARPS * 32), smem_bytes(1), st, tm_kv, tm_kr, p);
-    } else {
-        cudaError_t e = raise_smem_limit((const void *)grouped_decode_kernel<2>, smem_bytes(2));
-        if (e != cudaSuccess) return e;
-        MLA_STEP_LAUNCH(grouped_decode_kernel<2>, dim3(grid), dim3(WARPS * 32), smem_bytes(2), st, tm_kv, tm_kr, p);
-    }
+    const int rt = s_q <= 2 ? 1 : 2;
+    const bool win = view.kind == VIEW_WINDOW;
+    auto k = rt == 1 ? (win ? grouped_decode_kernel<1, true> : grouped_decode_kernel<1, false>)
+                     : (win ? grouped_decode_kernel<2, true> : grouped_decode_kernel<2, false>);
+    cudaError_t e = raise_smem_limit((const void *)k, smem_bytes(rt));
+    if (e != cudaSuccess) return e;
+    MLA_STEP_LAUNCH(k, dim3(grid), dim3(WARPS * 32), smem_bytes(rt), st, tm_kv, tm_kr, p);
     return cudaGetLastError();
 }
 

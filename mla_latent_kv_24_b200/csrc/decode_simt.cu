@@ -9,6 +9,9 @@
 // tiles of 32 tokens (one per lane) are staged in shared memory as fp32, every warp runs an
 // online softmax for its heads with warp-shuffle max/sum, and writes the unnormalised partial
 // output with its running max m and sum l for the combine kernel.
+//
+// With VIEW the item's tokens are those of a window or a tree (view.cuh): tokens it does not see
+// are staged as zeros, whatever their slots hold, and take no part in the softmax.
 #include <math.h>
 
 #include "kernels.h"
@@ -30,6 +33,8 @@ struct P {
     int *err;
     int H, hpw, HB, DK, DV, d_c, d_r, d_n, d_v, page, G, max_pages, n_pages, s_q;
     float scale;
+    View view;
+    const int *seq_lens;
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -43,7 +48,7 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-template <typename T, int MODE>
+template <typename T, int MODE, bool VIEW>
 __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
     step_begin();
     extern __shared__ float smem[];
@@ -64,6 +69,11 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
     const T *exq = (const T *)p.expanded;
 
     const int nh = min(p.HB, p.H - h0);  // heads of this CTA
+    ItemView iv;
+    if (VIEW) {
+        if (it.t1 > it.t0) iv = item_view(p.view, p.seq_lens, b, it.row % p.s_q, p.s_q, p.page);   // else a rejected plan
+    }
+    auto token = [&](int v) { return VIEW ? iv.token(v) : v; };
     for (int i = threadIdx.x; i < nh * p.DK; i += blockDim.x) {
         const int hh = i / p.DK, k = i % p.DK;
         qs[i] = to_f32(q[((size_t)it.row * p.H + h0 + hh) * p.DK + k]);
@@ -82,8 +92,8 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
     for (int tb = it.t0; tb < it.t1; tb += TT) {
         __syncthreads();
         if (threadIdx.x < TT) {
-            const int tok = tb + threadIdx.x;
-            int ok = tok < it.t1;
+            const int tok = token(tb + threadIdx.x);
+            int ok = tb + (int)threadIdx.x < it.t1 && (!VIEW || iv.seen(tok));
             if (ok) {
                 const int pid = p.page_table[(size_t)b * p.max_pages + tok / p.page];
                 if (pid < 0 || pid >= p.n_pages) {
@@ -101,7 +111,7 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
             const int okp = tok_ok[t];
             float v = 0.f;
             if (okp) {
-                const size_t pid = (size_t)(okp - 1), r = (size_t)((tb + t) % p.page);
+                const size_t pid = (size_t)(okp - 1), r = (size_t)(token(tb + t) % p.page);
                 if (MODE == 0) {
                     v = to_f32(lat[(pid * p.page + r) * d_row + k]);
                 } else {
@@ -117,7 +127,7 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
                 const int okp = tok_ok[t];
                 float v = 0.f;
                 if (okp) {
-                    const size_t pid = (size_t)(okp - 1), r = (size_t)((tb + t) % p.page);
+                    const size_t pid = (size_t)(okp - 1), r = (size_t)(token(tb + t) % p.page);
                     v = to_f32(exq[((pid * p.G + g) * p.page + r) * (p.d_n + p.d_v) + p.d_n + c]);
                 }
                 vs[t * VS + c] = v;
@@ -172,7 +182,7 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
 
 template <typename T, int MODE>
 cudaError_t launch_t(const P &p, dim3 grid, size_t smem, cudaStream_t st) {
-    auto k = decode_simt_kernel<T, MODE>;
+    auto k = p.view.kind == VIEW_CAUSAL ? decode_simt_kernel<T, MODE, false> : decode_simt_kernel<T, MODE, true>;
     cudaError_t e = raise_smem_limit((const void *)k, smem);
     if (e != cudaSuccess) return e;
     MLA_STEP_LAUNCH(k, dim3(grid), dim3(WARPS * 32), smem, st, p);
@@ -211,6 +221,8 @@ cudaError_t launch_decode_simt(const Dims &d, const SimtDecodeArgs &a, cudaStrea
     p.n_pages = a.n_pages;
     p.s_q = a.s_q;
     p.scale = d.scale;
+    p.view = a.view;
+    p.seq_lens = a.seq_lens;
     if (a.plan.n_work == 0) return cudaSuccess;
     dim3 grid(a.plan.n_work, ceil_div(d.H, p.HB));
     size_t smem = sizeof(float) * ((size_t)MAX_HB * p.DK + (size_t)TT * (p.DK + 1) +

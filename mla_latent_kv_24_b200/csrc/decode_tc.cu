@@ -74,9 +74,11 @@ enum {
     B_PFULL = B_SFREE + 2,
     B_PVDONE = B_PFULL + 2,
     B_OFREE = B_PVDONE + 2,
-    B_VLOCAL,   // this CTA's own copy of a ragged page's V tile (count 1, local)
-    B_VTAIL,    // both CTAs zeroed the stale rows of a ragged page's V tiles (count 2, leader)
-    B_COUNT
+    // One of each per page of the step, so that a page's copy and clearing never meet the phase of
+    // the other page's: the slot's next use waits for VEMPTY, i.e. for both.
+    B_VLOCAL,                // this CTA's own copy of a partly seen page's V tile (count 1, local)
+    B_VTAIL = B_VLOCAL + NV, // both CTAs zeroed the unseen rows of such a page's V tiles (count 2, leader)
+    B_COUNT = B_VTAIL + NV
 };
 constexpr uint32_t OFF_TMEMPTR = OFF_BAR + B_COUNT * 8;
 constexpr uint32_t OFF_FLAG = OFF_TMEMPTR + 8;
@@ -113,6 +115,8 @@ struct TcParams {
     int *err;
     uint64_t wait_ns;  // limit of every barrier wait (WAIT_NS unless a test shortens it)
     int withhold;      // test hook: the PV issuer skips the completion signal of this step (-1: none)
+    View view;
+    const int *seq_lens;   // views other than causal
 };
 
 struct Ctx {
@@ -153,11 +157,31 @@ __device__ __forceinline__ int item_of_round(const Plan &pl, int pair, int n_pai
     return pl.order ? pl.order[j] : j;
 }
 
-// Row coordinate (in the [n_pages*64, 576] view) of page index `pi` of request `b`; pages with
-// no token before `t_end` and out-of-range page ids read as zeros (coordinate past the end).
-__device__ __forceinline__ int page_row(const TcParams &p, int b, int pi, int t_end) {
-    if (pi * PAGE >= t_end) return p.n_pages * PAGE;
-    const int pid = p.page_table[(size_t)b * p.max_pages + pi];
+// What an item sees.  Causal rows see all of [t0, t1); with VIEW the item's tokens are virtual and
+// only some of a page may be seen (view.cuh).
+template <bool VIEW>
+struct Seen {
+    ItemView iv;
+    __device__ __forceinline__ Seen(const TcParams &p, const WorkItem &it) {
+        if (VIEW) iv = item_view(p.view, p.seq_lens, it.row / p.s_q, it.row % p.s_q, p.s_q, PAGE);
+    }
+    // Seen rows (bit = row) of the page that starts at (virtual) token v0.
+    __device__ __forceinline__ unsigned long long page(const WorkItem &it, int v0) const {
+        const int n = it.t1 - v0;
+        if (n <= 0) return 0ull;
+        if (VIEW) return iv.seen64(iv.token(v0));
+        return n >= PAGE ? ~0ull : (1ull << n) - 1ull;
+    }
+    __device__ __forceinline__ int token(int v) const { return VIEW ? iv.token(v) : v; }
+};
+
+// Row coordinate (in the [n_pages*64, 576] view) of the page at (virtual) token v0 of request `b`;
+// pages of which the item sees nothing and out-of-range page ids read as zeros (coordinate past
+// the end).
+template <bool VIEW>
+__device__ __forceinline__ int page_row(const TcParams &p, const Seen<VIEW> &sn, const WorkItem &it, int b, int v0) {
+    if (VIEW ? sn.page(it, v0) == 0ull : v0 >= it.t1) return p.n_pages * PAGE;
+    const int pid = p.page_table[(size_t)b * p.max_pages + sn.token(v0) / PAGE];
     if (pid < 0 || pid >= p.n_pages) {
         report(p.err, MLA_ERR_DEVICE_BOUNDS);
         return p.n_pages * PAGE;
@@ -176,6 +200,7 @@ __device__ __forceinline__ int page_row(const TcParams &p, int b, int pi, int t_
 // and slot 0 of an item's first step load in parallel), then per 128-token step K slots [j0, j1)
 // of the CTA's own page of the step.  Steps are numbered across
 // items (g), so every slot's phase is g's parity.
+template <bool VIEW>
 __device__ void run_k_producer(const Ctx &c, const TcParams &p, const CUtensorMap *tm_q, const CUtensorMap *tm_k,
                                int pair, int n_pairs, int j0, int j1) {
     int g = 0, item_n = 0;
@@ -184,7 +209,8 @@ __device__ void run_k_producer(const Ctx &c, const TcParams &p, const CUtensorMa
         if (it.t1 <= it.t0) continue;   // only in a rejected plan, and then for every item
         const int b = it.row / p.s_q;
         const int n_steps = ceil_div(it.t1 - it.t0, STEP);
-        auto own_row = [&](int i) { return page_row(p, b, (it.t0 + STEP * i) / PAGE + (int)c.rank, it.t1); };
+        const Seen<VIEW> sn(p, it);
+        auto own_row = [&](int i) { return page_row(p, sn, it, b, it.t0 + STEP * i + PAGE * (int)c.rank); };
         if (j1 == NK) {
             if (item_n > 0 && !wait_or_abort(c, c.bar(B_QEMPTY), (uint32_t)(item_n - 1) & 1u, p.err)) return;
             if (c.rank == 0) tc::mbar_arrive_expect_tx(c.bar(B_QFULL), 2u * Q_BYTES);
@@ -202,17 +228,14 @@ __device__ void run_k_producer(const Ctx &c, const TcParams &p, const CUtensorMa
     }
 }
 
-// Rows of the page starting at token `row0` that lie inside the item, when that is a proper part
-// of the page (the request's ragged last page): its other rows are slots past the request's length,
-// which may hold anything, NaN included.  0 otherwise.
-__device__ __forceinline__ int ragged_rows(const WorkItem &it, int row0) {
-    const int valid = it.t1 - row0;
-    return (valid > 0 && valid < PAGE) ? valid : 0;
-}
+// Whether an item sees a proper part of a page (the request's ragged last page, a window's first, a
+// tree's nodes): the other rows may hold anything, NaN included.
+__device__ __forceinline__ bool partly(unsigned long long seen) { return seen != 0ull && seen != ~0ull; }
 
 // V producer (lane 0): per step and page pg of the step, this CTA's 256 latent columns of that
-// page.  A ragged page is copied with this CTA's own barrier instead, and its stale rows are
+// page.  A partly seen page is copied with this CTA's own barrier instead, and its unseen rows are
 // cleared by run_v_tail.
+template <bool VIEW>
 __device__ void run_v_producer(const Ctx &c, const TcParams &p, const CUtensorMap *tm_v, int pair, int n_pairs) {
     int g = 0;
     for (int rnd = 0, k; (k = item_of_round(p.plan, pair, n_pairs, rnd)) >= 0; ++rnd) {
@@ -220,52 +243,62 @@ __device__ void run_v_producer(const Ctx &c, const TcParams &p, const CUtensorMa
         if (it.t1 <= it.t0) continue;
         const int b = it.row / p.s_q;
         const int n_steps = ceil_div(it.t1 - it.t0, STEP);
+        const Seen<VIEW> sn(p, it);
         for (int i = 0; i < n_steps; ++i, ++g) {
             const int t_step = it.t0 + STEP * i;
             for (int pg = 0; pg < NV; ++pg) {
-                const int y = page_row(p, b, t_step / PAGE + pg, it.t1);
+                const int y = page_row(p, sn, it, b, t_step + PAGE * pg);
                 if (!wait_or_abort(c, c.bar(B_VEMPTY + pg), ((uint32_t)g & 1u) ^ 1u, p.err)) return;
-                if (!ragged_rows(it, t_step + PAGE * pg)) {
+                if (!partly(sn.page(it, t_step + PAGE * pg))) {
                     if (c.rank == 0) tc::mbar_arrive_expect_tx(c.bar(B_VFULL + pg), 2u * VSLOT);
                     tc::tma_load_4d_pair(c.vslot(pg), tm_v, 0, y, 2 * (int)c.rank, 0, c.lead_bar(B_VFULL + pg));
                 } else {
                     // This phase of VFULL carries no bytes; the PV issuer waits on the tail barrier.
                     if (c.rank == 0) tc::mbar_arrive_expect_tx(c.bar(B_VFULL + pg), 0u);
-                    tc::mbar_arrive_expect_tx(c.bar(B_VLOCAL), VSLOT);
-                    tc::tma_load_4d(c.vslot(pg), tm_v, 0, y, 2 * (int)c.rank, 0, c.bar(B_VLOCAL));
+                    tc::mbar_arrive_expect_tx(c.bar(B_VLOCAL + pg), VSLOT);
+                    tc::tma_load_4d(c.vslot(pg), tm_v, 0, y, 2 * (int)c.rank, 0, c.bar(B_VLOCAL + pg));
                 }
             }
         }
     }
 }
 
-// Lanes 1-31 of the V producer's warp: for each ragged page, once its copy has landed, zero the
-// rows past the item's end in this CTA's V tile (their probabilities are zero, but 0 x NaN is
-// NaN in P.V), make the stores visible to the tensor core and report on the leader's tail
-// barrier.  Zeroing whole 128-byte rows of each 64-column block needs no knowledge of the
-// 128-byte swizzle.
+// Lanes 1-31 of the V producer's warp: for each partly seen page, once its copy has landed, zero
+// its unseen rows in this CTA's V tile (their probabilities are zero, but 0 x NaN is NaN in P.V),
+// make the stores visible to the tensor core and report on the leader's tail barrier.  Zeroing
+// whole 128-byte rows of each 64-column block needs no knowledge of the 128-byte swizzle.
+template <bool VIEW>
 __device__ void run_v_tail(const Ctx &c, const TcParams &p, int pair, int n_pairs) {
     const int lane = threadIdx.x % 32;   // 1..31
-    int nt = 0;                          // ragged pages so far (phase of B_VLOCAL)
+    uint32_t ph = 0;                     // bit pg: phase of B_VLOCAL + pg
     for (int rnd = 0, k; (k = item_of_round(p.plan, pair, n_pairs, rnd)) >= 0; ++rnd) {
         const WorkItem it = p.plan.items[k];
         if (it.t1 <= it.t0) continue;
         const int n_steps = ceil_div(it.t1 - it.t0, STEP);
-        for (int i = n_steps - 1; i < n_steps; ++i)   // only an item's last step can hold its end
+        const Seen<VIEW> sn(p, it);
+        for (int i = VIEW ? 0 : n_steps - 1; i < n_steps; ++i)   // a causal row's end is in its last step
             for (int pg = 0; pg < NV; ++pg) {
-                const int valid = ragged_rows(it, it.t0 + STEP * i + PAGE * pg);
-                if (!valid) continue;
-                const bool ok = wait_or_abort(c, c.bar(B_VLOCAL), (uint32_t)(nt++) & 1u, p.err);
+                const unsigned long long seen = sn.page(it, it.t0 + STEP * i + PAGE * pg);
+                if (!partly(seen)) continue;
+                const bool ok = wait_or_abort(c, c.bar(B_VLOCAL + pg), (ph >> pg) & 1u, p.err);
+                ph ^= 1u << pg;
                 if (!__all_sync(0xfffffffeu, ok)) return;
                 uint8_t *tile = c.sbase + OFF_V + VSLOT * pg;      // four [64 rows][128 B] blocks
-                const int n16 = (PAGE - valid) * 8;                // 16-byte pieces past the end, per block
-                for (int e = lane - 1; e < 4 * n16; e += 31) {
-                    const int blk = e / n16, r = e % n16;
-                    *reinterpret_cast<uint4 *>(tile + BOX * blk + 128 * valid + 16 * r) = make_uint4(0u, 0u, 0u, 0u);
+                if (!VIEW) {
+                    const int valid = it.t1 - (it.t0 + STEP * i + PAGE * pg);
+                    const int n16 = (PAGE - valid) * 8;            // 16-byte pieces past the end, per block
+                    for (int e = lane - 1; e < 4 * n16; e += 31) {
+                        const int blk = e / n16, r = e % n16;
+                        *reinterpret_cast<uint4 *>(tile + BOX * blk + 128 * valid + 16 * r) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                } else {
+                    for (int e = lane - 1; e < 4 * PAGE * 8; e += 31)
+                        if (!((seen >> (e / 8 % PAGE)) & 1ull))
+                            *reinterpret_cast<uint4 *>(tile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp(0xfffffffeu);
-                if (lane == 1) tc::mbar_arrive_cluster(c.lead_bar(B_VTAIL));
+                if (lane == 1) tc::mbar_arrive_cluster(c.lead_bar(B_VTAIL + pg));
             }
     }
 }
@@ -315,14 +348,17 @@ __device__ void run_qk_issuer(const Ctx &c, const TcParams &p, uint32_t tmem, in
     }
 }
 
+template <bool VIEW>
 __device__ void run_pv_issuer(const Ctx &c, const TcParams &p, uint32_t tmem, int pair, int n_pairs) {
-    int g = 0, item_n = 0, nt = 0;   // nt: ragged pages so far (phase of B_VTAIL)
+    int g = 0, item_n = 0;
+    uint32_t ph = 0;   // bit pg: phase of B_VTAIL + pg
     const uint64_t vdesc = tc::sdesc_sw128(c.base + OFF_V, BOX, 1024);
     const uint32_t o_tmem = tmem + TM_O;
     for (int rnd = 0, k; (k = item_of_round(p.plan, pair, n_pairs, rnd)) >= 0; ++rnd) {
         const WorkItem it = p.plan.items[k];
         if (it.t1 <= it.t0) continue;
         const int n_steps = ceil_div(it.t1 - it.t0, STEP);
+        const Seen<VIEW> sn(p, it);
         for (int i = 0; i < n_steps; ++i, ++g) {
             if (!wait_or_abort<true>(c, c.bar(B_PFULL + (g & 1)), (uint32_t)(g >> 1) & 1u, p.err)) return;
             // The first PV of an item overwrites O: the previous item's epilogue must be done with it.
@@ -332,9 +368,10 @@ __device__ void run_pv_issuer(const Ctx &c, const TcParams &p, uint32_t tmem, in
 #pragma unroll
             for (int pg = 0; pg < NV; ++pg) {
                 if (!wait_or_abort<true>(c, c.bar(B_VFULL + pg), (uint32_t)g & 1u, p.err)) return;
-                if (ragged_rows(it, it.t0 + STEP * i + PAGE * pg) &&
-                    !wait_or_abort<true>(c, c.bar(B_VTAIL), (uint32_t)(nt++) & 1u, p.err))
-                    return;
+                if (partly(sn.page(it, it.t0 + STEP * i + PAGE * pg))) {
+                    if (!wait_or_abort<true>(c, c.bar(B_VTAIL + pg), (ph >> pg) & 1u, p.err)) return;
+                    ph ^= 1u << pg;
+                }
                 tc::fence_after_sync();
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch)
@@ -362,6 +399,7 @@ __device__ void run_pv_issuer(const Ctx &c, const TcParams &p, uint32_t tmem, in
 // and, at the end, their sums through shared memory behind a named barrier.  Control flow does
 // not depend on data or on a wait's outcome: a wait that runs out only records the error, so
 // every thread always reaches every named barrier.
+template <bool VIEW>
 __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int pair, int n_pairs) {
     const int t = threadIdx.x;                     // 0..255
     const int warp = t / 32, lane = t % 32;
@@ -390,6 +428,7 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
             continue;
         }
         const int n_steps = ceil_div(it.t1 - it.t0, STEP);
+        const Seen<VIEW> sn(p, it);
         float m_run = -INFINITY, l_run = 0.f;
         for (int i = 0; i < n_steps; ++i, ++g) {
             const int sb = g & 1;
@@ -404,10 +443,11 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
 
             const int tok0 = it.t0 + STEP * i + 64 * hsel + 32 * half;
             const int nvalid = min(32, max(0, it.t1 - tok0));
+            const uint32_t seen = VIEW ? (uint32_t)(sn.page(it, tok0 - 32 * half) >> (32 * half)) : 0u;
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                s[j] = j < nvalid ? s[j] : -INFINITY;
+                s[j] = (VIEW ? (seen >> j) & 1u : j < nvalid) ? s[j] : -INFINITY;
                 m4[j & 3] = fmaxf(m4[j & 3], s[j]);
             }
             float o1, o2, o3;
@@ -427,7 +467,8 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
                 m_run = m_tile;
             } else if (any) {
                 const float m_new = fmaxf(m_run, m_tile);
-                const float alpha = tc::ex2(m_run - m_new);
+                // With a view a row may not have seen anything yet (O and l are zero then).
+                const float alpha = VIEW && m_run == -INFINITY ? (m_new == -INFINITY ? 1.f : 0.f) : tc::ex2(m_run - m_new);
 #pragma unroll 1
                 for (int q = 0; q < 2; ++q) {
                     float v[64];
@@ -442,7 +483,7 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
                 l_run *= alpha;
                 m_run = m_new;
             }
-            const float neg_m = -m_run;
+            const float neg_m = VIEW && m_run == -INFINITY ? 0.f : -m_run;
             float sum4[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t pk[16];
 #pragma unroll
@@ -516,6 +557,7 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
     }
 }
 
+template <bool VIEW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, TcParams p) {
@@ -558,8 +600,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc::mbar_init(c.bar(B_PFULL), 2 * SOFTMAX_WARPS);
         tc::mbar_init(c.bar(B_PFULL + 1), 2 * SOFTMAX_WARPS);
         tc::mbar_init(c.bar(B_OFREE), 2 * SOFTMAX_WARPS);
-        tc::mbar_init(c.bar(B_VLOCAL), 1);
-        tc::mbar_init(c.bar(B_VTAIL), 2);
+        for (int i = 0; i < NV; ++i) {
+            tc::mbar_init(c.bar(B_VLOCAL + i), 1);
+            tc::mbar_init(c.bar(B_VTAIL + i), 2);
+        }
         *c.abort_flag = 0;
         tc::fence_mbar_init();
     }
@@ -578,20 +622,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
     const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
     if (warp == W_KPROD) {
-        if (lane == 0) run_k_producer(c, p, &tm_q, &tm_k, pair, n_pairs, 0, K_SPLIT);
+        if (lane == 0) run_k_producer<VIEW>(c, p, &tm_q, &tm_k, pair, n_pairs, 0, K_SPLIT);
     } else if (warp == W_KPROD2) {
-        if (lane == 0) run_k_producer(c, p, &tm_q, &tm_k, pair, n_pairs, K_SPLIT, NK);
+        if (lane == 0) run_k_producer<VIEW>(c, p, &tm_q, &tm_k, pair, n_pairs, K_SPLIT, NK);
     } else if (warp == W_VPROD) {
         if (lane == 0)
-            run_v_producer(c, p, &tm_v, pair, n_pairs);
+            run_v_producer<VIEW>(c, p, &tm_v, pair, n_pairs);
         else
-            run_v_tail(c, p, pair, n_pairs);
+            run_v_tail<VIEW>(c, p, pair, n_pairs);
     } else if (warp == W_MMA) {
         if (c.rank == 0 && lane == 0) run_qk_issuer(c, p, tmem, pair, n_pairs);
     } else if (warp == W_PV) {
-        if (c.rank == 0 && lane == 0) run_pv_issuer(c, p, tmem, pair, n_pairs);
+        if (c.rank == 0 && lane == 0) run_pv_issuer<VIEW>(c, p, tmem, pair, n_pairs);
     } else {
-        run_softmax(c, p, tmem, pair, n_pairs);
+        run_softmax<VIEW>(c, p, tmem, pair, n_pairs);
     }
 
     if (*c.abort_flag) {
@@ -700,7 +744,7 @@ int tc_token_granule() { return STEP; }
 
 cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *latent, const int *page_table,
                              const Plan &plan, int max_pages, int n_pages, int s_q, float *part_o, float *part_ml,
-                             int *err, int sms, cudaStream_t st) {
+                             int *err, int sms, cudaStream_t st, const View &view, const int *seq_lens) {
     if (plan.n_work == 0) return cudaSuccess;
     CUtensorMap tm_q, tm_k, tm_v;
     const uint64_t kv_rows = (uint64_t)n_pages * PAGE;
@@ -719,10 +763,13 @@ cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *laten
     p.err = err;
     p.wait_ns = g_test_wait_ns;
     p.withhold = g_test_withhold;
-    cudaError_t e = raise_smem_limit((const void *)tc_decode_kernel, SMEM_ALLOC);
+    p.view = view;
+    p.seq_lens = seq_lens;
+    auto k = view.kind == VIEW_CAUSAL ? tc_decode_kernel<false> : tc_decode_kernel<true>;
+    cudaError_t e = raise_smem_limit((const void *)k, SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     const int units = std::max(1, std::min(plan.n_work, std::max(1, sms / 2)));
-    MLA_STEP_LAUNCH(tc_decode_kernel, dim3(2 * units), dim3(THREADS), SMEM_ALLOC, st, tm_q, tm_k, tm_v, p);
+    MLA_STEP_LAUNCH(k, dim3(2 * units), dim3(THREADS), SMEM_ALLOC, st, tm_q, tm_k, tm_v, p);
     return cudaGetLastError();
 }
 

@@ -13,6 +13,15 @@
 
 namespace mla {
 
+// Tokens of plan row r: a causal row's visible ones, or the window's or tree's virtual length
+// (view.cuh), negative for lengths that cannot be.
+__device__ __forceinline__ int plan_row_len(const PlanArgs &a, int r) {
+    const int b = r / a.s_q, j = r % a.s_q, L = a.seq_lens[b];
+    if (a.view.kind == VIEW_CAUSAL) return L - a.s_q + j + 1;
+    return view_row_len(a.view.kind, a.view.sinks, a.view.window, L, a.view.kind == VIEW_TREE ? a.view.n_nodes[b] : 0,
+                        a.s_q, a.n_q, j, a.page, a.max_pages * a.page);
+}
+
 // `scratch` is shared memory of the calling block (2 * cap_rows + 1 ints, the block's own
 // buffers, which the plan block does not otherwise use): batches of at most cap_rows rows keep
 // the row starts and lengths there, so the block's dependent reads (the binary searches of the
@@ -33,10 +42,9 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
     __syncthreads();
     int local = 0;
     for (int r = r0; r < r1; ++r) {
-        const int b = r / a.s_q, j = r % a.s_q;
-        const int L = a.seq_lens[b];
-        if (L < a.s_q || L > a.max_pages * a.page) atomicOr(&bad, 1);
-        const int len = L - a.s_q + j + 1;
+        const int L = a.seq_lens[r / a.s_q];
+        const int len = plan_row_len(a, r);
+        if (a.view.kind == VIEW_CAUSAL ? L < a.s_q || L > a.max_pages * a.page : len < 0) atomicOr(&bad, 1);
         if (in_smem) s_len[r] = len;
         local += len > 0 ? ceil_div(len, a.chunk) : 0;
     }
@@ -73,10 +81,9 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
     }
     int k = first;
     for (int r = r0; r < r1; ++r) {
-        const int b = r / a.s_q, j = r % a.s_q;
         a.row_first[r] = k;
         if (in_smem) s_first[r] = k;
-        k += ceil_div(in_smem ? s_len[r] : a.seq_lens[b] - a.s_q + j + 1, a.chunk);
+        k += ceil_div(in_smem ? s_len[r] : plan_row_len(a, r), a.chunk);
     }
     if (threadIdx.x == PT - 1) {
         a.row_first[rows] = a.n_expected;
@@ -98,9 +105,8 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
         __syncthreads();
         int lp = 0;   // rows of this thread that end in a shorter chunk
         for (int r = r0; r < r1; ++r) {
-            const int b = r / a.s_q, j = r % a.s_q;
-            const int len = in_smem ? s_len[r] : a.seq_lens[b] - a.s_q + j + 1;
-            const int last = len - (ceil_div(len, a.chunk) - 1) * a.chunk;
+            const int len = in_smem ? s_len[r] : plan_row_len(a, r);
+            const int last = len - (ceil_div(len, a.chunk) - 1) * a.chunk;   // = chunk for an empty row
             if (last < a.chunk) {
                 ++lp;
                 atomicAdd(&o_hist[min(OB - 1, (int)((long long)last * OB / a.chunk))], 1);
@@ -130,8 +136,7 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
         int pr = warp_sum[warp] + inc - lp;
         for (int r = r0; r < r1; ++r) {
             P[r] = pr;
-            const int b = r / a.s_q, j = r % a.s_q;
-            const int len = in_smem ? s_len[r] : a.seq_lens[b] - a.s_q + j + 1;
+            const int len = in_smem ? s_len[r] : plan_row_len(a, r);
             if (len - (ceil_div(len, a.chunk) - 1) * a.chunk < a.chunk) ++pr;
         }
         if (threadIdx.x == 0) {
@@ -152,8 +157,7 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
             if (rf[mid] <= i) lo = mid;
             else hi = mid - 1;
         }
-        const int b = lo / a.s_q, j = lo % a.s_q;
-        const int len = in_smem ? s_len[lo] : a.seq_lens[b] - a.s_q + j + 1;
+        const int len = in_smem ? s_len[lo] : plan_row_len(a, lo);
         const int c = i - rf[lo];
         a.items[i] = WorkItem{lo, c * a.chunk, min(len, (c + 1) * a.chunk), c};
         if (a.order) {

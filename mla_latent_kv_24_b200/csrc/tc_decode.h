@@ -12,7 +12,8 @@ int tc_units(int sms);        // concurrent workers the split plan should cover
 int tc_token_granule();       // chunk lengths are multiples of this many tokens
 cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *latent, const int *page_table,
                              const Plan &plan, int max_pages, int n_pages, int s_q, float *part_o,
-                             float *part_ml, int *err, int sms, cudaStream_t st);
+                             float *part_ml, int *err, int sms, cudaStream_t st, const View &view = View{},
+                             const int *seq_lens = nullptr);   // seq_lens: for the views other than causal
 
 // Test hook of the bounded waits: later tcgen05 decodes on the calling thread skip the completion
 // signal of pipeline step `withhold_step` (-1: none) and give up every wait after `wait_ns`
@@ -36,6 +37,7 @@ cudaError_t launch_prefill_tc(const Dims &d, const void *q_rot, const void *expa
                               int n_pages, int n_q, float *part_o, float *part_ml, int *err, cudaStream_t st);
 cudaError_t launch_grouped_decode(const Dims &d, const void *q, const void *expanded, const void *latent,
                                   const int *seq_lens, const int *page_table, const Plan &plan, int max_pages,
-                                  int n_pages, int s_q, float *part_o, float *part_ml, int *err, cudaStream_t st);
+                                  int n_pages, int s_q, float *part_o, float *part_ml, int *err, cudaStream_t st,
+                                  const View &view = View{});   // causal or window
 
 }  // namespace mla

@@ -41,7 +41,7 @@ expanded and grouped forms, RoPE identities, and the pages' cache-size arithmeti
 from .mla import (  # noqa: F401
     rope_frequencies, rope, down_project, slot_of, request_rows,
     attention_weights, decode_request_expanded, decode_expanded,
-    decode_request_absorbed, expand_group_cache, decode_request_grouped,
+    decode_request_masked, decode_request_absorbed, expand_group_cache, decode_request_grouped,
     partial_attention, combine_partials, cache_append,
     mha_scalars_per_token, mla_scalars_per_token, gqa_scalars_per_token,
     gqa_path_bytes_per_token, absorbed_path_bytes_per_token,

@@ -143,6 +143,27 @@ def decode_request_expanded(q_b: np.ndarray, rows: np.ndarray, W_uk: np.ndarray,
     return out
 
 
+def decode_request_masked(q_b: np.ndarray, rows: np.ndarray, W_uk: np.ndarray, W_uv: np.ndarray, hpw: int,
+                          scale: float, base: float, positions: Sequence[int], visible: np.ndarray) -> np.ndarray:
+    """Head-expanded MLA attention with any mask: query j of q_b [n, H, d_n + d_r] sits at positions[j] and
+    sees the rows [L, d_c + d_r] where visible[j] [L] is true.  A query that sees nothing gives zeros; a row
+    that it does not see has no part in its result, whatever it holds.  Returns [n, H, d_v]."""
+    n, H, _ = q_b.shape
+    d_n, d_c, d_v = W_uk.shape[1], W_uk.shape[2], W_uv.shape[1]
+    out = np.zeros((n, H, d_v), dtype=F64)
+    r = np.asarray(rows, dtype=F64)
+    seen = [np.flatnonzero(visible[j]) for j in range(n)]
+    for w in range(H // hpw):
+        K = np.concatenate([r[:, :d_c] @ np.asarray(W_uk[w], F64).T, r[:, d_c:]], axis=1)
+        V = r[:, :d_c] @ np.asarray(W_uv[w], F64).T
+        for h in range(w * hpw, (w + 1) * hpw):
+            for j in range(n):
+                if len(seen[j]):
+                    q = _q_tilde(q_b[j, h].astype(F64), d_n, positions[j], base)
+                    out[j, h] = attention_weights(q, K[seen[j]], len(seen[j]) - 1, scale) @ V[seen[j]]
+    return out
+
+
 def decode_expanded(q, W_uk, W_uv, cache, page_table, seq_lens, hpw: int, scale: float, base: float,
                     sample: Optional[Sequence[Tuple[int, int, int]]] = None) -> np.ndarray:
     """Whole-batch decode out [B, s_q, H, d_v]; with ``sample`` = [(b, j, h), ...] only those

@@ -366,3 +366,44 @@ def test_no_max_subtraction_overflows():
     with np.errstate(over="ignore", invalid="ignore"):
         bad = _bad_weights_no_max(np.array([1.0, 0.0]), K, 2, 1e4)
     assert not np.array_equal(bad, [0.0, 0.0, 1.0])
+
+
+# ----------------------------------------------------------------------------- any mask
+def _masked(p, b, positions, visible):
+    rows = om.request_rows(p["cache"], p["page_table"], b, int(p["seq_lens"][b]))
+    return om.decode_request_masked(p["q"][b], rows, p["W_uk"], p["W_uv"], p["hpw"], p["scale"], p["base"], positions,
+                                    visible)
+
+
+def test_masked_form_with_the_causal_mask_is_the_expanded_form():
+    p = _rand_problem(np.random.default_rng(50))
+    ref = _oracle_out(p)
+    for b, L in enumerate(p["seq_lens"]):
+        pos = [int(L) - p["s_q"] + j for j in range(p["s_q"])]
+        got = _masked(p, b, pos, np.arange(L)[None] <= np.asarray(pos)[:, None])
+        assert np.abs(got - ref[b]).max() <= 1e-12
+
+
+def test_masked_form_sees_what_the_mask_says():
+    # a single visible token gives its value; a query that sees nothing gives zeros; a row that a query
+    # does not see may hold anything; and a subset is the brute force over that subset's tokens
+    rng = np.random.default_rng(51)
+    p = _rand_problem(rng, B=1, lens=(9,))
+    rows = om.request_rows(p["cache"], p["page_table"], 0, 9)
+    vis = np.zeros((2, 9), bool)
+    vis[0, 4] = True
+    rows[7] = np.nan
+    got = om.decode_request_masked(p["q"][0], rows, p["W_uk"], p["W_uv"], p["hpw"], p["scale"], p["base"], [3, 8], vis)
+    for h in range(4):
+        assert np.abs(got[0, h] - p["W_uv"][h // 2] @ rows[4, :p["d_c"]]).max() <= 1e-12
+    assert (got[1] == 0).all()
+    pick = [0, 2, 5, 8]
+    vis = np.zeros((2, 9), bool)
+    vis[:, pick] = True
+    got = om.decode_request_masked(p["q"][0], rows, p["W_uk"], p["W_uv"], p["hpw"], p["scale"], p["base"], [2, 3], vis)
+    # the brute force over the four rows alone places its last two queries at positions 2 and 3 too; its
+    # first one does not see the fourth row
+    ref = np.asarray(brute.decode(p["q"].tolist(), p["W_uk"].tolist(), p["W_uv"].tolist(), [rows[pick].tolist()], 2,
+                                  p["hpw"], p["d_c"], p["d_n"], p["scale"], p["base"]))
+    assert np.abs(got[1] - ref[0, 1]).max() <= 1e-12
+    assert np.abs(got[0] - ref[0, 0]).max() > 1e-3
