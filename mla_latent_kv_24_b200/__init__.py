@@ -136,6 +136,9 @@ def _dev(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # 0.1 us; the Stream object costs 3
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -268,47 +271,54 @@ def mla_debug_decode_fault(withhold_step: int, wait_us: int = 0) -> None:
 # caller's structures, so their types, sizes and device are checked here: a short or narrow one
 # would be read past its end.
 # ---------------------------------------------------------------------------------------
-def _arr(name, t, itemsize, n, optional=False) -> Optional[int]:
-    """Device address of a contiguous tensor of at least n elements of `itemsize` bytes on the current device."""
+def _here() -> int:
+    """The current device; one that no tensor is on while CUDA has not been used."""
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _arr(name, t, itemsize, n, here, optional=False) -> Optional[int]:
+    """Device address of a contiguous tensor of at least n elements of `itemsize` bytes on device `here`."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is None")
-    p = _dev(t)
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    if t.element_size() != itemsize:
-        raise ValueError(f"{name} has {t.element_size()}-byte elements, expected {itemsize}")
-    if t.numel() < n:
+    if t.get_device() != here or t.itemsize != itemsize or t.numel() < n or not t.is_contiguous():
+        _dev(t)
+        if t.get_device() != here:
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+        if t.itemsize != itemsize:
+            raise ValueError(f"{name} has {t.itemsize}-byte elements, expected {itemsize}")
         raise ValueError(f"{name} has {t.numel()} elements, expected at least {n}")
-    return p
+    return t.data_ptr()
 
 
 def _host_lens(name, x, n):
-    a, p = _host_i32(x)
+    """(array that keeps the memory, address) of a host int32 array of at least n elements."""
+    a = x if type(x) is np.ndarray and x.dtype == np.int32 and x.flags.c_contiguous else \
+        np.ascontiguousarray(np.asarray(x, dtype=np.int32))
     if a.size < n:
         raise ValueError(f"{name} has {a.size} elements, expected at least {n}")
-    return a, p
+    return a, a.ctypes.data
 
 
-def _decode_view_args(dims, q, s_q, cache, n_pages_total, batch, max_pages, page_table, seq_lens, out):
+def _decode_view_args(dims, q, s_q, cache, n_pages_total, batch, max_pages, page_table, seq_lens, out, here):
     e = 4 if dims.dtype == MLA_FP32 else 2
     rows = batch * s_q * dims.n_heads
-    return e, (_arr("q", q, e, rows * (dims.d_nope + dims.d_rope)),
-               _arr("latent_cache", cache, e, n_pages_total * dims.page_size * (dims.d_c + dims.d_rope)),
-               _arr("page_table", page_table, 4, batch * max_pages), _arr("seq_lens", seq_lens, 4, batch),
-               _arr("out", out, e, rows * dims.d_v))
+    return e, (_arr("q", q, e, rows * (dims.d_nope + dims.d_rope), here),
+               _arr("latent_cache", cache, e, n_pages_total * dims.page_size * (dims.d_c + dims.d_rope), here),
+               _arr("page_table", page_table, 4, batch * max_pages, here), _arr("seq_lens", seq_lens, 4, batch, here),
+               _arr("out", out, e, rows * dims.d_v, here))
 
 
-def _weights(dims, e, W_uk, W_uv):
+def _weights(dims, e, W_uk, W_uv, here):
     g = dims.n_heads // max(1, dims.heads_per_group)
-    return _arr("W_uk", W_uk, e, g * dims.d_nope * dims.d_c), _arr("W_uv", W_uv, e, g * dims.d_v * dims.d_c)
+    return _arr("W_uk", W_uk, e, g * dims.d_nope * dims.d_c, here), _arr("W_uv", W_uv, e, g * dims.d_v * dims.d_c, here)
 
 
-def _workspace(ws, nbytes):
-    have = ws.numel() * ws.element_size()
-    return _arr("workspace", ws, ws.element_size(), 0), have if nbytes is None else min(nbytes, have)
+def _workspace(ws, nbytes, here):
+    have = ws.numel() * ws.itemsize
+    return _arr("workspace", ws, ws.itemsize, 0, here), have if nbytes is None else min(nbytes, have)
 
 
 def mla_decode_tree_workspace_size(dims, batch, max_nodes, seq_lens_host, n_nodes_host) -> int:
@@ -326,30 +336,34 @@ def mla_decode_tree(dims, q, W_uk, W_uv, latent_cache, page_table, seq_lens, n_n
     int64 (or uint64) tensor of bit masks; see include/mla.h."""
     lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
     nodes, np_ = _host_lens("n_nodes_host", n_nodes_host, batch)
+    here = _here()
     e, (qp, cp, tp, sp, op) = _decode_view_args(dims, q, max_nodes, latent_cache, n_pages_total, batch, max_pages,
-                                                page_table, seq_lens, out)
-    uk, uv = _weights(dims, e, W_uk, W_uv)
-    ws, nbytes = _workspace(workspace, workspace_bytes)
-    _check(load().mla_decode_tree(ctypes.byref(dims), qp, uk, uv, cp, tp, sp, _arr("n_nodes", n_nodes, 4, batch), lp,
-                                  np_, _arr("depths", depths, 4, batch * max_nodes),
-                                  _arr("tree_mask", tree_mask, 8, batch * max_nodes), batch, max_nodes, max_pages,
+                                                page_table, seq_lens, out, here)
+    uk, uv = _weights(dims, e, W_uk, W_uv, here)
+    ws, nbytes = _workspace(workspace, workspace_bytes, here)
+    _check(load().mla_decode_tree(ctypes.byref(dims), qp, uk, uv, cp, tp, sp,
+                                  _arr("n_nodes", n_nodes, 4, batch, here), lp, np_,
+                                  _arr("depths", depths, 4, batch * max_nodes, here),
+                                  _arr("tree_mask", tree_mask, 8, batch * max_nodes, here), batch, max_nodes, max_pages,
                                   n_pages_total, op, ws, nbytes, _stream(stream)))
 
 
 def mla_decode_window_workspace_size(dims, batch, s_q, sinks, window, seq_lens_host) -> int:
     lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
     out = _S(0)
-    _check(load().mla_decode_window_workspace_size(ctypes.byref(dims), batch, s_q, sinks, window, lp, ctypes.byref(out)))
+    _check(load().mla_decode_window_workspace_size(ctypes.byref(dims), batch, s_q, sinks, window, lp,
+                                                   ctypes.byref(out)))
     return out.value
 
 
 def mla_decode_window(dims, q, W_uk, W_uv, latent_cache, page_table, seq_lens, seq_lens_host, batch, s_q, sinks,
                       window, max_pages, n_pages_total, out, workspace, workspace_bytes=None, stream=None) -> None:
     lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    here = _here()
     e, (qp, cp, tp, sp, op) = _decode_view_args(dims, q, s_q, latent_cache, n_pages_total, batch, max_pages,
-                                                page_table, seq_lens, out)
-    uk, uv = _weights(dims, e, W_uk, W_uv)
-    ws, nbytes = _workspace(workspace, workspace_bytes)
+                                                page_table, seq_lens, out, here)
+    uk, uv = _weights(dims, e, W_uk, W_uv, here)
+    ws, nbytes = _workspace(workspace, workspace_bytes, here)
     _check(load().mla_decode_window(ctypes.byref(dims), qp, uk, uv, cp, tp, sp, lp, batch, s_q, sinks, window,
                                     max_pages, n_pages_total, op, ws, nbytes, _stream(stream)))
 
@@ -365,11 +379,12 @@ def gqla_decode_window_workspace_size(dims, batch, s_q, sinks, window, seq_lens_
 def gqla_decode_window(dims, q, expanded_cache, latent_cache, page_table, seq_lens, seq_lens_host, batch, s_q, sinks,
                        window, max_pages, n_pages_total, out, workspace, workspace_bytes=None, stream=None) -> None:
     lens, lp = _host_lens("seq_lens_host", seq_lens_host, batch)
+    here = _here()
     e, (qp, cp, tp, sp, op) = _decode_view_args(dims, q, s_q, latent_cache, n_pages_total, batch, max_pages,
-                                                page_table, seq_lens, out)
+                                                page_table, seq_lens, out, here)
     g = dims.n_heads // max(1, dims.heads_per_group)
-    ep = _arr("expanded_cache", expanded_cache, e, n_pages_total * g * dims.page_size * (dims.d_nope + dims.d_v))
-    ws, nbytes = _workspace(workspace, workspace_bytes)
+    ep = _arr("expanded_cache", expanded_cache, e, n_pages_total * g * dims.page_size * (dims.d_nope + dims.d_v), here)
+    ws, nbytes = _workspace(workspace, workspace_bytes, here)
     _check(load().gqla_decode_window(ctypes.byref(dims), qp, ep, cp, tp, sp, lp, batch, s_q, sinks, window, max_pages,
                                      n_pages_total, op, ws, nbytes, _stream(stream)))
 
@@ -377,59 +392,64 @@ def gqla_decode_window(dims, q, expanded_cache, latent_cache, page_table, seq_le
 def mla_cache_append_slots(dims, h, hidden, W_dkv, W_kr, req_idx, slots, positions, n_tok, page_table, batch,
                            max_pages, n_pages_total, latent_cache, stream=None) -> None:
     e = 4 if dims.dtype == MLA_FP32 else 2
-    row = dims.d_c + dims.d_rope
+    row, here = dims.d_c + dims.d_rope, _here()
     _check(load().mla_cache_append_slots(
-        ctypes.byref(dims), _arr("h", h, e, n_tok * hidden), hidden, _arr("W_dkv", W_dkv, e, dims.d_c * hidden, True),
-        _arr("W_kr", W_kr, e, dims.d_rope * hidden, True), _arr("req_idx", req_idx, 4, n_tok),
-        _arr("slots", slots, 4, n_tok), _arr("positions", positions, 4, n_tok), n_tok,
-        _arr("page_table", page_table, 4, batch * max_pages), batch, max_pages, n_pages_total,
-        _arr("latent_cache", latent_cache, e, n_pages_total * dims.page_size * row), _stream(stream)))
+        ctypes.byref(dims), _arr("h", h, e, n_tok * hidden, here), hidden,
+        _arr("W_dkv", W_dkv, e, dims.d_c * hidden, here, True),
+        _arr("W_kr", W_kr, e, dims.d_rope * hidden, here, True), _arr("req_idx", req_idx, 4, n_tok, here),
+        _arr("slots", slots, 4, n_tok, here), _arr("positions", positions, 4, n_tok, here), n_tok,
+        _arr("page_table", page_table, 4, batch * max_pages, here), batch, max_pages, n_pages_total,
+        _arr("latent_cache", latent_cache, e, n_pages_total * dims.page_size * row, here), _stream(stream)))
 
 
-def _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, refs_optional=False):
-    return (_arr("seq_lens", seq_lens, 4, batch), _arr("page_table", page_table, 4, batch * max_pages),
-            _arr("page_refs", page_refs, 4, n_pages_total, refs_optional))
+def _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here, refs_optional=False):
+    return (_arr("seq_lens", seq_lens, 4, batch, here), _arr("page_table", page_table, 4, batch * max_pages, here),
+            _arr("page_refs", page_refs, 4, n_pages_total, here, refs_optional))
 
 
-def _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total):
+def _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total, here):
     e = 4 if dims.dtype == MLA_FP32 else 2
     rows = n_layers * n_pages_total * dims.page_size
     g = dims.n_heads // max(1, dims.heads_per_group)
-    return (_arr("latent_cache", latent_cache, e, rows * (dims.d_c + dims.d_rope), True),
-            _arr("expanded_cache", expanded_cache, e, rows * g * (dims.d_nope + dims.d_v), True))
+    return (_arr("latent_cache", latent_cache, e, rows * (dims.d_c + dims.d_rope), here, True),
+            _arr("expanded_cache", expanded_cache, e, rows * g * (dims.d_nope + dims.d_v), here, True))
 
 
 def mla_cache_reserve(dims, new_lens, seq_lens, page_table, batch, max_pages, page_refs, n_pages_total,
                       stream=None) -> None:
-    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total)
-    _check(load().mla_cache_reserve(ctypes.byref(dims), _arr("new_lens", new_lens, 4, batch), s, t, batch, max_pages,
-                                    r, n_pages_total, _stream(stream)))
+    here = _here()
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here)
+    _check(load().mla_cache_reserve(ctypes.byref(dims), _arr("new_lens", new_lens, 4, batch, here), s, t, batch,
+                                    max_pages, r, n_pages_total, _stream(stream)))
 
 
 def mla_cache_fork(dims, src_req, dst_req, n_fork, seq_lens, page_table, batch, max_pages, page_refs, n_pages_total,
                    latent_cache, expanded_cache, n_layers, stream=None) -> None:
-    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total)
-    lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total)
-    _check(load().mla_cache_fork(ctypes.byref(dims), _arr("src_req", src_req, 4, n_fork),
-                                 _arr("dst_req", dst_req, 4, n_fork), n_fork, s, t, batch, max_pages, r,
+    here = _here()
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here)
+    lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total, here)
+    _check(load().mla_cache_fork(ctypes.byref(dims), _arr("src_req", src_req, 4, n_fork, here),
+                                 _arr("dst_req", dst_req, 4, n_fork, here), n_fork, s, t, batch, max_pages, r,
                                  n_pages_total, lat, exp, n_layers, _stream(stream)))
 
 
 def mla_cache_release(dims, req_idx, first_page, last_page, n_req, seq_lens, page_table, batch, max_pages, page_refs,
                       n_pages_total, stream=None) -> None:
-    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total)
-    _check(load().mla_cache_release(ctypes.byref(dims), _arr("req_idx", req_idx, 4, n_req),
-                                    _arr("first_page", first_page, 4, n_req, True),
-                                    _arr("last_page", last_page, 4, n_req, True), n_req, s, t, batch, max_pages, r,
-                                    n_pages_total, _stream(stream)))
+    here = _here()
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here)
+    _check(load().mla_cache_release(ctypes.byref(dims), _arr("req_idx", req_idx, 4, n_req, here),
+                                    _arr("first_page", first_page, 4, n_req, here, True),
+                                    _arr("last_page", last_page, 4, n_req, here, True), n_req, s, t, batch, max_pages,
+                                    r, n_pages_total, _stream(stream)))
 
 
 def mla_cache_accept(dims, ctx_lens, n_nodes, accepted, n_accepted, max_nodes, seq_lens, page_table, batch, max_pages,
                      page_refs, n_pages_total, latent_cache, expanded_cache, n_layers, stream=None) -> None:
-    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, True)
-    lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total)
-    _check(load().mla_cache_accept(ctypes.byref(dims), _arr("ctx_lens", ctx_lens, 4, batch),
-                                   _arr("n_nodes", n_nodes, 4, batch),
-                                   _arr("accepted", accepted, 4, batch * max_nodes),
-                                   _arr("n_accepted", n_accepted, 4, batch), max_nodes, s, t, batch, max_pages, r,
+    here = _here()
+    s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here, True)
+    lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total, here)
+    _check(load().mla_cache_accept(ctypes.byref(dims), _arr("ctx_lens", ctx_lens, 4, batch, here),
+                                   _arr("n_nodes", n_nodes, 4, batch, here),
+                                   _arr("accepted", accepted, 4, batch * max_nodes, here),
+                                   _arr("n_accepted", n_accepted, 4, batch, here), max_nodes, s, t, batch, max_pages, r,
                                    n_pages_total, lat, exp, n_layers, _stream(stream)))

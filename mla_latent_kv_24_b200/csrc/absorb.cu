@@ -66,8 +66,12 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
     }
 }
 
-// GQA path: the no-position part is used as is; only the RoPE part turns.
+// GQA path: the no-position part is used as is; only the RoPE part turns.  A warp takes RH heads of a
+// row: each lane forms one pair's angle, sine and cosine (in double) once for all of them.  (One angle
+// per head and pair, as before, kept the double-precision units busy for 7 us at 4 rows and 16 at 64.)
 // The last block builds the split plan instead.
+constexpr int RH = 8;
+
 template <typename T>
 __global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, const int *__restrict__ seq_lens,
                                                      int rows, int s_q, int H, int d_r, int d_n, float base,
@@ -78,25 +82,37 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, co
         plan_block<256>(plan, scratch, 512);
         return;
     }
-    const int d_qk = d_n + d_r;
-    const size_t n = (size_t)rows * H * (d_qk / 2);
-    const size_t stride = (size_t)(gridDim.x - 1) * blockDim.x;
-    for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n; i += stride) {
-        const int pr = (int)(i % (d_qk / 2));
-        const size_t rh = i / (d_qk / 2);
-        const int row = (int)(rh / H);
-        const T *src = q + rh * d_qk + 2 * pr;
-        T *dst = q_rot + rh * d_qk + 2 * pr;
-        if (2 * pr < d_n) {
-            dst[0] = src[0];
-            dst[1] = src[1];
-        } else {
-            const int b = row / s_q, j = row % s_q, p = seq_lens[b] - s_q + j;
-            float x0 = to_f32(src[0]), x1 = to_f32(src[1]), cs, sn;
-            rope_cos_sin(p, (2 * pr - d_n) / 2, d_r, base, &cs, &sn);
-            dst[0] = from_f32<T>(x0 * cs - x1 * sn);
-            dst[1] = from_f32<T>(x0 * sn + x1 * cs);
+    const int d_qk = d_n + d_r, groups = ceil_div(H, RH), lane = threadIdx.x % 32;
+    const long long n = (long long)rows * groups;
+    const long long stride = (long long)(gridDim.x - 1) * (blockDim.x / 32);
+    struct alignas(2 * sizeof(T)) Pair {
+        T a, b;
+    };
+    const int quads = d_n * (int)sizeof(T) / 16;   // 16-byte pieces of a head's no-position part
+    for (long long u = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; u < n; u += stride) {
+        const int row = (int)(u / groups), h0 = (int)(u % groups) * RH, nh = min(H - h0, RH);
+        const int b = row / s_q, j = row % s_q, p = seq_lens[b] - s_q + j;
+        const T *src = q + ((size_t)row * H + h0) * d_qk;
+        T *dst = q_rot + ((size_t)row * H + h0) * d_qk;
+        const bool turns = 2 * lane < d_r;
+        Pair x[RH];
+#pragma unroll
+        for (int h = 0; h < RH; ++h)
+            if (turns && h < nh) x[h] = *reinterpret_cast<const Pair *>(src + (size_t)h * d_qk + d_n + 2 * lane);
+#pragma unroll 4
+        for (int i = lane; i < nh * quads; i += 32) {
+            const int h = i / quads, c = i % quads;
+            reinterpret_cast<uint4 *>(dst + (size_t)h * d_qk)[c] = reinterpret_cast<const uint4 *>(src + (size_t)h * d_qk)[c];
         }
+        float cs = 0.f, sn = 0.f;
+        if (turns) rope_cos_sin(p, lane, d_r, base, &cs, &sn);
+#pragma unroll
+        for (int h = 0; h < RH; ++h)
+            if (turns && h < nh) {
+                const float x0 = to_f32(x[h].a), x1 = to_f32(x[h].b);
+                *reinterpret_cast<Pair *>(dst + (size_t)h * d_qk + d_n + 2 * lane) =
+                    Pair{from_f32<T>(x0 * cs - x1 * sn), from_f32<T>(x0 * sn + x1 * cs)};
+            }
     }
 }
 
@@ -119,8 +135,8 @@ cudaError_t launch_q_absorb(const Dims &d, const void *q, const void *W_uk, cons
 cudaError_t launch_q_rope(const Dims &d, const void *q, const int *seq_lens, int batch, int s_q, void *q_rot,
                           const PlanArgs &plan, cudaStream_t st) {
     const int rows = batch * s_q;
-    const size_t n = (size_t)rows * d.H * ((d.d_n + d.d_r) / 2);
-    const int blocks = (int)std::min<size_t>((n + 255) / 256, 4096) + 1;   // + the plan block
+    const size_t n = (size_t)rows * ceil_div(d.H, RH);
+    const int blocks = (int)std::min<size_t>((n + 7) / 8, 4096) + 1;   // + the plan block
     if (d.bf16)
         MLA_STEP_LAUNCH(q_rope_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, st, (const __nv_bfloat16 *)q,
                         seq_lens, rows, s_q, d.H, d.d_r, d.d_n, d.base, (__nv_bfloat16 *)q_rot, plan);
@@ -135,58 +151,70 @@ cudaError_t launch_q_rope(const Dims &d, const void *q, const int *seq_lens, int
 // ---------------------------------------------------------------------------------------
 // Tensor-core q absorption for the DeepSeek-V2 shape (bf16, d_nope = 128, d_c = 512,
 // d_rope = 64).  Per head it is the GEMM q_lat[rows, 512] = q_nope[rows, 128] W_UK[w]
-// ([128, 512], row k = nope dim).  One CTA computes 64 query rows x 128 latent columns of one
-// head with mma.sync m16n8k16: the W_UK tile [128 k][64 n] and the q tile [64][128] are staged
-// in padded shared memory by cp.async, B fragments come through ldmatrix.trans.  Every W_UK
-// element is read once per head (16.8 MB in total for H = 128), the bound of this step.
-// CTAs of the first column tile also rotate the query's RoPE part.
+// ([128, 512], row k = nope dim), with mma.sync m16n8k16: the W_UK tile [128 k][n] and the q tile are
+// staged in padded shared memory by cp.async, B fragments come through ldmatrix.trans.  Every W_UK
+// element is read once per head (16.8 MB in total for H = 128), the bound of this step for a few rows;
+// for many it is the 147 KB written per row.
+//
+// Two forms.  Up to 16 rows one CTA computes 16 rows x 128 columns of one head, so that a decode step's
+// whole grid (4 column tiles per head) is one wave of CTAs: a CTA stores only after the previous kernel
+// has completed, and a second wave would start its loads only then.  More rows: a CTA keeps its W_UK
+// tile (128 columns) and walks 64-row tiles of the batch, the next tile's queries arriving while this
+// one is multiplied, and stores whole 256-byte row pieces through shared memory.  (With 64 x 64 tiles
+// of their own and 4-byte stores: 82 us for 512 rows, 29 for 128; this form PLACEHOLDER.)
+//
+// The extra columns of blocks build the split plan (their first block) and turn the queries' RoPE part:
+// a warp takes 16 heads of a row, so that each pair's double-precision angle is formed once for them
+// (forming it for every head took a third of the 512-row time).
 // ---------------------------------------------------------------------------------------
 #include "warp_mma.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int AB_K = 128, AB_LD = AB_K + 8;
+constexpr int AB_K = 128, AB_LD = AB_K + 8, AB_N = 128, AB_LDB = AB_N + 8;
+constexpr int D_C = 512, D_N = 128, D_R = 64, D_QK = 192, D_OUT = 576;
+constexpr int ROPE_WARPS = 8;   // warps of a row: each takes every eighth head
 
-// TM query rows x TN latent columns of one head per CTA; eight warps as (TM / 16) row tiles x
-// (8 / (TM / 16)) column groups.  Small batches take 16 x 128 tiles, so that a decode step's
-// whole grid (4 column tiles per head) is one wave of CTAs: a CTA stores only after the previous
-// kernel has completed, and a second wave would start its loads only then.
-template <int TM, int TN>
-__global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *__restrict__ q,
-                                                           const __nv_bfloat16 *__restrict__ W_uk,
-                                                           const int *__restrict__ seq_lens, int rows, int s_q,
-                                                           int H, int hpw, float base,
-                                                           __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
-    constexpr int LDB = TN + 8, WM = TM / 16, WN = 8 / WM, CW = TN / WN, NT = CW / 8;
-    static_assert(TM % 16 == 0 && 8 % WM == 0 && NT % 2 == 0, "warp tiling");
-    step_allow_next();   // loads and products touch inputs only; every store waits (below)
-    __shared__ __align__(16) __nv_bfloat16 As[TM * AB_LD];     // [rows][128 k]
-    __shared__ __align__(16) __nv_bfloat16 Bs[AB_K * LDB];     // [128 k][TN n]
-    if (blockIdx.x == H) {   // the extra column of blocks: its first block builds the split plan
-        constexpr int CAP = ((int)sizeof(Bs) / 4 - 1) / 2;      // row starts and lengths in Bs
-        if (blockIdx.y == 0 && blockIdx.z == 0) plan_block<256>(plan, reinterpret_cast<int *>(Bs), CAP);
+// Blocks past the heads' (see above); `id` counts them.
+__device__ __forceinline__ void absorb_extra_block(int id, const __nv_bfloat16 *__restrict__ q,
+                                                   const int *__restrict__ seq_lens, int rows, int s_q, int H, float base,
+                                                   __nv_bfloat16 *__restrict__ q_abs, const PlanArgs &plan, int *scratch,
+                                                   int cap) {
+    if (id == 0) {
+        plan_block<256>(plan, scratch, cap);
         return;
     }
-    const int h = blockIdx.x, n0 = blockIdx.y * TN, row0 = blockIdx.z * TM;
-    const int w = h / hpw, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    constexpr int D_C = 512, D_N = 128, D_R = 64, D_QK = 192, D_OUT = 576;
-    const __nv_bfloat16 *Wk = W_uk + (size_t)w * D_N * D_C;
-    for (int c = tid; c < AB_K * TN / 8; c += 256) {            // 16-byte chunks of the W_UK tile
-        const int k = c / (TN / 8), n = (c % (TN / 8)) * 8;
-        cp_async16(Bs + k * LDB + n, Wk + (size_t)k * D_C + n0 + n, true);
+    const int row = id - 1, lane = threadIdx.x % 32, first = threadIdx.x / 32;
+    if (row >= rows) {
+        step_wait_prev();
+        return;
     }
-    for (int c = tid; c < TM * AB_K / 8; c += 256) {
-        const int r = c / (AB_K / 8), k = (c % (AB_K / 8)) * 8;
-        const int row = row0 + r;
-        cp_async16(As + r * AB_LD + k, q + ((size_t)(row < rows ? row : 0) * H + h) * D_QK + k, row < rows);
+    constexpr int U = 16;
+    const int b = row / s_q, j = row % s_q;
+    const __nv_bfloat16 *src = q + (size_t)row * H * D_QK + D_N + 2 * lane;
+    __nv_bfloat16 *dst = q_abs + (size_t)row * H * D_OUT + D_C + 2 * lane;
+    uint32_t x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = first + ROPE_WARPS * u;
+        x[u] = h < H ? *reinterpret_cast<const uint32_t *>(src + (size_t)h * D_QK) : 0u;
     }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    // warp tile: 16 rows x CW columns (NT n8 tiles)
-    const int wm = warp % WM, wn = warp / WM;
-    float acc[NT][4];
+    float cs, sn;
+    rope_cos_sin(query_pos(plan.view, seq_lens, b, j, s_q), lane, D_R, base, &cs, &sn);
+    step_wait_prev();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {   // H <= 128 = U ROPE_WARPS
+        const int h = first + ROPE_WARPS * u;
+        const float x0 = __uint_as_float(x[u] << 16), x1 = __uint_as_float(x[u] & 0xffff0000u);
+        if (h < H) *reinterpret_cast<uint32_t *>(dst + (size_t)h * D_OUT) = pack_bf16(x0 * cs - x1 * sn, x0 * sn + x1 * cs);
+    }
+}
+
+// One warp's 16 x (8 NT) product of the staged tiles.
+template <int NT>
+__device__ __forceinline__ void absorb_mma(float (*acc)[4], const __nv_bfloat16 *As, const __nv_bfloat16 *Bs, int m0, int n0,
+                                           int lane) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -194,42 +222,123 @@ __global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *
 #pragma unroll
     for (int kk = 0; kk < AB_K; kk += 16) {
         uint32_t a[4];
-        ldmatrix_x4(a[0], a[1], a[2], a[3],
-                    As + (wm * 16 + (lane % 8) + 8 * ((lane / 8) % 2)) * AB_LD + kk + 8 * (lane / 16));
+        ldmatrix_x4(a[0], a[1], a[2], a[3], As + (m0 + (lane % 8) + 8 * ((lane / 8) % 2)) * AB_LD + kk + 8 * (lane / 16));
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
             // B stored [k][n]: .trans gives the k-major fragments of two n8 tiles
             uint32_t b0, b1, b2, b3;
             const int kr = kk + (lane % 8) + 8 * ((lane / 8) % 2);
-            const int nc = wn * CW + j * 8 + 8 * (lane / 16);
-            ldmatrix_x4_trans(b0, b1, b2, b3, Bs + kr * LDB + nc);
+            const int nc = n0 + j * 8 + 8 * (lane / 16);
+            ldmatrix_x4_trans(b0, b1, b2, b3, Bs + kr * AB_LDB + nc);
             mma_bf16(acc[j], a, b0, b1);
             mma_bf16(acc[j + 1], a, b2, b3);
         }
     }
+}
+
+__device__ __forceinline__ void absorb_load_w(__nv_bfloat16 *Bs, const __nv_bfloat16 *Wk, int n0) {
+    for (int c = threadIdx.x; c < AB_K * AB_N / 8; c += 256) {   // 16-byte chunks of the W_UK tile
+        const int k = c / (AB_N / 8), n = (c % (AB_N / 8)) * 8;
+        cp_async16(Bs + k * AB_LDB + n, Wk + (size_t)k * D_C + n0 + n, true);
+    }
+}
+template <int TM>
+__device__ __forceinline__ void absorb_load_q(__nv_bfloat16 *As, const __nv_bfloat16 *q, int row0, int rows, int H, int h) {
+    for (int c = threadIdx.x; c < TM * AB_K / 8; c += 256) {
+        const int r = c / (AB_K / 8), k = (c % (AB_K / 8)) * 8, row = row0 + r;
+        cp_async16(As + r * AB_LD + k, q + ((size_t)(row < rows ? row : 0) * H + h) * D_QK + k, row < rows);
+    }
+}
+
+// Up to 16 rows: grid (H + extra, 4).
+__global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *__restrict__ q,
+                                                           const __nv_bfloat16 *__restrict__ W_uk,
+                                                           const int *__restrict__ seq_lens, int rows, int s_q,
+                                                           int H, int hpw, float base,
+                                                           __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
+    step_allow_next();   // loads and products touch inputs only; every store waits (below)
+    __shared__ __align__(16) __nv_bfloat16 As[16 * AB_LD];          // [rows][128 k]
+    __shared__ __align__(16) __nv_bfloat16 Bs[AB_K * AB_LDB];       // [128 k][128 n]
+    const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
+    if (h >= H) {
+        absorb_extra_block((h - H) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base, q_abs, plan,
+                           reinterpret_cast<int *>(Bs), ((int)sizeof(Bs) / 4 - 1) / 2);
+        return;
+    }
+    absorb_load_w(Bs, W_uk + (size_t)(h / hpw) * D_N * D_C, n0);
+    absorb_load_q<16>(As, q, 0, rows, H, h);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float acc[2][4];
+    absorb_mma<2>(acc, As, Bs, 0, 16 * warp, lane);
     const int gid = lane / 4, t4 = lane % 4;
     step_wait_prev();   // q_abs is workspace the previous call's kernels may still read
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
-        const int row = row0 + wm * 16 + gid + 8 * hr;
+        const int row = gid + 8 * hr;
         if (row >= rows) continue;
-        __nv_bfloat16 *dst = q_abs + ((size_t)row * H + h) * D_OUT + n0 + wn * CW;
+        __nv_bfloat16 *dst = q_abs + ((size_t)row * H + h) * D_OUT + n0 + 16 * warp;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < 2; ++j)
             *reinterpret_cast<uint32_t *>(dst + j * 8 + 2 * t4) = pack_bf16(acc[j][2 * hr], acc[j][2 * hr + 1]);
     }
-    if (blockIdx.y == 0) {   // RoPE part of the query, rows of this tile
-        for (int i = tid; i < TM * (D_R / 2); i += 256) {
-            const int r = i / (D_R / 2), pi = i % (D_R / 2), row = row0 + r;
-            if (row >= rows) continue;
-            const int b = row / s_q, j = row % s_q, pos = query_pos(plan.view, seq_lens, b, j, s_q);
-            const __nv_bfloat16 *src = q + ((size_t)row * H + h) * D_QK + D_N + 2 * pi;
-            float x0 = __bfloat162float(src[0]), x1 = __bfloat162float(src[1]), cs, sn;
-            rope_cos_sin(pos, pi, D_R, base, &cs, &sn);
-            __nv_bfloat16 *o = q_abs + ((size_t)row * H + h) * D_OUT + D_C + 2 * pi;
-            o[0] = __float2bfloat16_rn(x0 * cs - x1 * sn);
-            o[1] = __float2bfloat16_rn(x0 * sn + x1 * cs);
+}
+
+// More rows: grid (H + extra, 4, z); a CTA takes the 64-row tiles blockIdx.z, blockIdx.z + z, ...
+constexpr int ABR = 64;
+constexpr size_t AB_ROWS_SMEM = sizeof(__nv_bfloat16) * (AB_K * AB_LDB + 2 * ABR * AB_LD);
+
+__global__ void __launch_bounds__(256, 3) q_absorb_rows_kernel(const __nv_bfloat16 *__restrict__ q,
+                                                               const __nv_bfloat16 *__restrict__ W_uk,
+                                                               const int *__restrict__ seq_lens, int rows, int s_q,
+                                                               int H, int hpw, float base,
+                                                               __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
+    step_allow_next();
+    extern __shared__ __align__(16) uint8_t absm[];
+    __nv_bfloat16 *Bs = reinterpret_cast<__nv_bfloat16 *>(absm);    // [128 k][128 n]
+    __nv_bfloat16 *As = Bs + AB_K * AB_LDB;                         // [2][64 rows][128 k]; a tile's output too
+    const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
+    if (h >= H) {
+        absorb_extra_block(((h - H) * gridDim.z + blockIdx.z) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base,
+                           q_abs, plan, reinterpret_cast<int *>(Bs), (AB_K * AB_LDB / 2 - 1) / 2);
+        return;
+    }
+    const int tiles = ceil_div(rows, ABR), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int gid = lane / 4, t4 = lane % 4, m0 = 16 * (warp % 4), c0 = 64 * (warp / 4);
+    absorb_load_w(Bs, W_uk + (size_t)(h / hpw) * D_N * D_C, n0);
+    absorb_load_q<ABR>(As, q, blockIdx.z * ABR, rows, H, h);
+    cp_async_commit();
+    int buf = 0;
+    for (int t = blockIdx.z; t < tiles; t += gridDim.z, buf ^= 1) {
+        __nv_bfloat16 *A = As + buf * ABR * AB_LD;
+        if (t + (int)gridDim.z < tiles) {
+            absorb_load_q<ABR>(As + (buf ^ 1) * ABR * AB_LD, q, (t + gridDim.z) * ABR, rows, H, h);
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
         }
+        __syncthreads();
+        float acc[8][4];
+        absorb_mma<8>(acc, A, Bs, m0, c0, lane);
+        __syncthreads();   // the queries are read: their tile takes the output
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint32_t *>(A + (m0 + gid + 8 * hr) * AB_LD + c0 + 8 * j + 2 * t4) =
+                    pack_bf16(acc[j][2 * hr], acc[j][2 * hr + 1]);
+        __syncthreads();
+        step_wait_prev();   // q_abs is workspace the previous call's kernels may still read
+        for (int c = threadIdx.x; c < ABR * AB_N / 8; c += 256) {
+            const int r = c / (AB_N / 8), n = (c % (AB_N / 8)) * 8, row = t * ABR + r;
+            if (row < rows)
+                *reinterpret_cast<uint4 *>(q_abs + ((size_t)row * H + h) * D_OUT + n0 + n) =
+                    *reinterpret_cast<const uint4 *>(A + r * AB_LD + n);
+        }
+        __syncthreads();   // the tile after next arrives here
     }
 }
 
@@ -240,14 +349,20 @@ bool q_absorb_mma_ok(const Dims &d) { return d.bf16 && d.d_n == 128 && d.d_c == 
 cudaError_t launch_q_absorb_mma(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch,
                                 int s_q, void *q_abs, const PlanArgs &plan, cudaStream_t st) {
     const int rows = batch * s_q;
+    constexpr int Y = D_C / AB_N;
     if (rows <= 16) {
-        dim3 grid(d.H + 1, 512 / 128, 1);   // + one column for the plan block
-        MLA_STEP_LAUNCH(q_absorb_mma_kernel<16, 128>, dim3(grid), dim3(256), 0, st, (const __nv_bfloat16 *)q,
+        dim3 grid(d.H + ceil_div(1 + rows, Y), Y, 1);
+        MLA_STEP_LAUNCH(q_absorb_mma_kernel, grid, dim3(256), 0, st, (const __nv_bfloat16 *)q,
                         (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs,
                         plan);
     } else {
-        dim3 grid(d.H + 1, 512 / 64, ceil_div(rows, 64));
-        MLA_STEP_LAUNCH(q_absorb_mma_kernel<64, 64>, dim3(grid), dim3(256), 0, st, (const __nv_bfloat16 *)q,
+        // Two tiles per CTA: enough to hide the queries' loads, short enough to share the SMs evenly.
+        const int z = std::min(ceil_div(ceil_div(rows, ABR), 2), 65535);
+        const long long per = (long long)Y * z;
+        dim3 grid(d.H + (unsigned)((rows + per) / per), Y, z);   // + blocks for the plan and `rows` RoPE rows
+        cudaError_t e = raise_smem_limit((const void *)q_absorb_rows_kernel, AB_ROWS_SMEM);
+        if (e != cudaSuccess) return e;
+        MLA_STEP_LAUNCH(q_absorb_rows_kernel, grid, dim3(256), AB_ROWS_SMEM, st, (const __nv_bfloat16 *)q,
                         (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs,
                         plan);
     }

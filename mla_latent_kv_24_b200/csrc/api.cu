@@ -189,7 +189,7 @@ mla_status make_layout(const Dims &d, Path path, bool tc, int sms, int batch, in
         units = tc_units(sms);
         granule = tc_token_granule();
     } else if (path == GROUPED && grouped_tc_ok(d, s_q)) {
-        units = grouped_units(d, sms);
+        units = grouped_units(d, sms, hv.v.kind == VIEW_WINDOW);
         granule = grouped_token_granule();
     } else {
         const int hb = simt_heads_per_block(d, path == ABSORBED ? 0 : 1);
@@ -415,10 +415,12 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
             MLA_CUDA(launch_plan(pa, st), "launch plan");
             MLA_CUDA(launch_q_absorb(d, q, W_uk, seq_lens, batch, s_q, qp, st, hv.v), "launch q_absorb");
         }
+        // A view's rows are merged by the kernel that suits their number, each from its own layout.
+        const bool oct = tc && (hv.v.kind == VIEW_CAUSAL || !combine_by_head(L.rows));
         if (tc) {
             ProfileScope prof(st);
             MLA_CUDA(launch_tc_decode(d, qp, latent, page_table, plan, max_pages, n_pages, s_q, part_o, part_ml, err, sms,
-                                      st, hv.v, seq_lens),
+                                      st, hv.v, seq_lens, oct),
                      "launch tcgen05 decode");
         } else {
             ProfileScope prof(st);
@@ -438,7 +440,8 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                 }
                 if (starts[L.rows] == L.n_work) sp = starts;
             }
-            MLA_CUDA(launch_combine_mma(d, part_o, part_ml, row_first, sp, L.rows, tc, W_uv, out, st, keep_empty),
+            MLA_CUDA(launch_combine_mma(d, part_o, part_ml, row_first, sp, L.rows, oct, W_uv, out, st,
+                                        keep_empty, hv.v.kind != VIEW_CAUSAL),
                      "launch combine + W_UV (tensor cores)");
         }
         else if (!tc)
@@ -801,7 +804,7 @@ static mla_status cache_rows(const Dims &d, void *latent, void *expanded, int32_
     if (n_layers < 1) return fail(MLA_ERR_INVALID_ARG, "n_layers must be > 0");
     if (!aligned16(latent) || !aligned16(expanded))
         return fail(MLA_ERR_INVALID_ARG, "device tensors must be 16-byte aligned");
-    if ((long long)n_layers * (expanded ? d.n_groups() : 1) > 65535) return fail(MLA_ERR_UNSUPPORTED, "n_layers too large");
+    if (n_layers > 65535) return fail(MLA_ERR_UNSUPPORTED, "n_layers must be <= 65535");
     auto add = [&](void *base, int pieces, size_t row) {
         const size_t piece = row * d.page, page = piece * pieces;
         const int vec = row % 16 == 0 ? 16 : row % 4 == 0 ? 4 : 2;

@@ -9,6 +9,8 @@
 // Rows of the caches are copied with 16-byte accesses (2 or 4 bytes where a row's size asks for it).
 // All of it is bound by launches and latency, except forks over many layers, which are bound by the
 // copied bytes.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kernels.h"
@@ -70,14 +72,13 @@ __device__ __forceinline__ uint32_t free_bits(const int *refs, int n_pages, int 
 
 // Hands the `wanted` lowest free pages to take(rank, page), rank 0 first, and marks them held.
 // False, with nothing changed, if there are fewer.  All PT threads call it.
+// first_tile: this thread's free_bits() of the first pages, which the caller loads ahead of its own chain.
 template <typename Take>
-__device__ __forceinline__ bool allocate(int *refs, int n_pages, int wanted, const Take &take) {
+__device__ __forceinline__ bool allocate(int *refs, int n_pages, int wanted, uint32_t first_tile, const Take &take) {
     int have = 0;
-    uint32_t first_tile = 0;
     for (int base = 0; base < n_pages && have < wanted; base += PT * PER) {
         const int at = base + (int)threadIdx.x * PER;
-        const uint32_t m = at < n_pages ? free_bits(refs, n_pages, at) : 0u;
-        if (base == 0) first_tile = m;
+        const uint32_t m = base == 0 ? first_tile : at < n_pages ? free_bits(refs, n_pages, at) : 0u;
         int total;
         block_prefix(__popc(m), &total);
         have += total;
@@ -99,6 +100,11 @@ __device__ __forceinline__ bool allocate(int *refs, int n_pages, int wanted, con
     return true;
 }
 
+struct RowSets {
+    PageRows r[2];
+    int n;
+};
+
 struct Pool {
     int *seq_lens, *page_table, *refs;
     int batch, max_pages, n_pages, page;
@@ -108,10 +114,16 @@ struct Pool {
     __device__ __forceinline__ int *entry(int b, int k) const { return page_table + (size_t)b * max_pages + k; }
 };
 
+__device__ __forceinline__ uint32_t first_bits(const Pool &p) {
+    const int at = (int)threadIdx.x * PER;
+    return at < p.n_pages ? free_bits(p.refs, p.n_pages, at) : 0u;
+}
+
 // ------------------------------------------------------------------------------------- reserve
 __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restrict__ new_lens) {
     step_begin();
     __shared__ int off[CAP + 1];
+    const uint32_t tile = first_bits(p);
     const int per = ceil_div(p.batch, PT), b0 = min(p.batch, (int)threadIdx.x * per), b1 = min(p.batch, b0 + per);
     int mine = 0, bad = 0;
     for (int b = b0; b < b1; ++b) {
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restri
         if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
         return;
     }
-    const bool ok = allocate(p.refs, p.n_pages, total, [&](int rank, int pg) {
+    const bool ok = allocate(p.refs, p.n_pages, total, tile, [&](int rank, int pg) {
         int lo = 0, hi = p.batch - 1;   // the last request that starts at or before `rank`
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
@@ -158,12 +170,12 @@ __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restri
 // ------------------------------------------------------------------------------------- fork
 // Checks and new pages.  Claims the destinations (which must be empty, each named once) by a compare
 // and swap of their length, so that a destination named twice is found whatever the order.  A call
-// that is carried out leaves -1 - length in every destination, which tells the copying blocks so;
-// fork_finish_kernel turns it into the length.
+// that is carried out leaves -1 - length in every destination, which tells the copying blocks so.
 __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
                                                        int n) {
     step_begin();
     __shared__ int len[CAP];
+    const uint32_t tile = first_bits(p);
     const int per = ceil_div(n, PT), i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
     int parts = 0, bad = 0;
     for (int i = i0; i < i1; ++i) {
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__rest
         first_rank[threadIdx.x] = rank0;
         if (threadIdx.x == PT - 1) first_rank[PT] = total;
         __syncthreads();
-        ok = allocate(p.refs, p.n_pages, total, [&](int rank, int pg) {
+        ok = allocate(p.refs, p.n_pages, total, tile, [&](int rank, int pg) {
             int lo = 0, hi = PT - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
@@ -215,7 +227,7 @@ __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__rest
     if (!ok && threadIdx.x == 0) report(p.err, bad ? MLA_ERR_DEVICE_BOUNDS : MLA_ERR_NO_PAGES);
 }
 
-// Shares the full pages (block 0 of a fork) and copies the partial page's rows of one piece.
+// Copies bytes [from, to) of a span with the block's threads.
 template <typename V>
 __device__ __forceinline__ void copy_span(char *dst, const char *src, size_t bytes) {
     const size_t n = bytes / sizeof(V);
@@ -232,42 +244,52 @@ __device__ __forceinline__ void copy_span(char *dst, const char *src, size_t byt
     for (; i < n; i += stride) reinterpret_cast<V *>(dst)[i] = reinterpret_cast<const V *>(src)[i];
 }
 
-constexpr int COPY_BYTES = 16384;   // of a piece per block
-
-template <typename V>
+// One cluster per fork shares the full pages and copies the partial page's rows, then gives the
+// destination its length.  A piece of rows goes to one block, or in parts to several when there are
+// fewer pieces than blocks.
 __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
-                                                        PageRows rows, int share) {
+                                                        RowSets sets) {
     step_begin();
-    const int s = src[blockIdx.x], d = dst[blockIdx.x];
-    if (s < 0 || s >= p.batch || d < 0 || d >= p.batch) return;   // reported by the plan
-    const int L = -1 - p.seq_lens[d];
-    if (L <= 0) return;                                           // refused as a whole, or an empty source
-    const int full = L / p.page, rem = L % p.page;
-    if (share && blockIdx.y == 0 && blockIdx.z == 0)
-        for (int k = threadIdx.x; k < full; k += blockDim.x) {
+    const int rank = blockIdx.x, blocks = gridDim.x;              // the cluster spans the grid's x
+    const int s = src[blockIdx.y], d = dst[blockIdx.y];
+    int L = 0;
+    if (s >= 0 && s < p.batch && d >= 0 && d < p.batch) L = -1 - p.seq_lens[d];   // <= 0: refused as a whole, or empty
+    if (L > 0) {
+        const int full = L / p.page, rem = L % p.page;
+        for (int k = rank * (int)blockDim.x + (int)threadIdx.x; k < full; k += blocks * (int)blockDim.x) {
             const int pg = *p.entry(s, k);
             *p.entry(d, k) = pg;
             if (pg >= p.n_pages) report(p.err, MLA_ERR_DEVICE_BOUNDS);
             else if (pg >= 0) atomicAdd(p.refs + pg, 1);          // a dropped page (< 0) has no holder to add
         }
-    if (!rem || !rows.base) return;
-    const int from = *p.entry(s, full), to = *p.entry(d, full);
-    if (from < 0 || from >= p.n_pages) {
-        if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
-        return;
+        if (rem && sets.n) {
+            const int from = *p.entry(s, full), to = *p.entry(d, full);
+            if (from < 0 || from >= p.n_pages) {
+                if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i >= sets.n) break;
+                    const PageRows &r = sets.r[i];
+                    const int units = r.n_layers * r.pieces, parts = units >= blocks ? 1 : ceil_div(blocks, units);
+                    const size_t bytes = (size_t)rem * r.row_bytes;
+                    const size_t part = ((bytes + parts - 1) / parts + 15) / 16 * 16;
+                    for (int w = rank; w < units * parts; w += blocks) {
+                        const size_t at = (size_t)(w % parts) * part;
+                        if (at >= bytes) continue;
+                        const size_t n = bytes - at < part ? bytes - at : part;
+                        char *to_p = r.at(w / parts, to) + at;
+                        const char *from_p = r.at(w / parts, from) + at;
+                        if (r.vec == 16) copy_span<uint4>(to_p, from_p, n);
+                        else if (r.vec == 4) copy_span<uint32_t>(to_p, from_p, n);
+                        else copy_span<uint16_t>(to_p, from_p, n);
+                    }
+                }
+            }
+        }
     }
-    const size_t bytes = (size_t)rem * rows.row_bytes, at = (size_t)blockIdx.z * COPY_BYTES;
-    if (at >= bytes) return;
-    const size_t n = bytes - at < (size_t)COPY_BYTES ? bytes - at : (size_t)COPY_BYTES;
-    copy_span<V>(rows.at(blockIdx.y, to) + at, rows.at(blockIdx.y, from) + at, n);
-}
-
-__global__ void __launch_bounds__(256) fork_finish_kernel(Pool p, const int *__restrict__ dst, int n) {
-    step_begin();
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n || dst[i] < 0 || dst[i] >= p.batch) return;
-    const int x = p.seq_lens[dst[i]];
-    if (x < 0) p.seq_lens[dst[i]] = -1 - x;
+    cooperative_groups::this_cluster().sync();   // every block has read the length's marker
+    if (rank == 0 && threadIdx.x == 0 && d >= 0 && d < p.batch && s >= 0 && s < p.batch && L >= 0) p.seq_lens[d] = L;
 }
 
 // ------------------------------------------------------------------------------------- release
@@ -312,7 +334,7 @@ __global__ void __launch_bounds__(256) release_kernel(Pool p, const int *__restr
 
 // ------------------------------------------------------------------------------------- accept
 // Whether request b's accepted path is one: node indices that rise and exist, in pages that it has.
-// The same answer in both kernels of a call.  All threads of the block call it.
+// The same answer in every block of a call.  All threads of the block call it.
 __device__ __forceinline__ bool path_ok(const Pool &p, int b, int ctx, int n, const int *acc, int n_acc, int max_nodes) {
     int bad = 0;
     if (n < 0 || n > max_nodes || n_acc < 0 || n_acc > n || ctx < 0 || (long long)ctx + n > (long long)p.max_pages * p.page)
@@ -331,53 +353,68 @@ __device__ __forceinline__ bool path_ok(const Pool &p, int b, int ctx, int n, co
 
 // Row acc[k] of the nodes moves to row k.  The indices rise, so acc[k] >= k: a thread that takes one
 // column of every row in order never reads a row that it has overwritten, and needs no buffer.
+struct Moves {
+    int from_page[MLA_MAX_TREE_NODES], from_row[MLA_MAX_TREE_NODES], to_page[MLA_MAX_TREE_NODES], to_row[MLA_MAX_TREE_NODES];
+};
 template <typename V>
-__global__ void __launch_bounds__(128) accept_move_kernel(Pool p, const int *__restrict__ ctx_lens,
-                                                          const int *__restrict__ n_nodes, const int *__restrict__ accepted,
-                                                          const int *__restrict__ n_accepted, int max_nodes,
-                                                          PageRows rows, int units) {
-    step_begin();
-    const int b = blockIdx.y;
-    const int ctx = ctx_lens[b], n = n_nodes[b], n_acc = n_accepted[b];
-    const int *acc = accepted + (size_t)b * max_nodes;
-    if (!path_ok(p, b, ctx, n, acc, n_acc, max_nodes)) return;   // reported by the kernel that follows
-    __shared__ int from_page[MLA_MAX_TREE_NODES], from_row[MLA_MAX_TREE_NODES], to_page[MLA_MAX_TREE_NODES],
-        to_row[MLA_MAX_TREE_NODES], n_move;
-    if (threadIdx.x == 0) n_move = 0;
-    __syncthreads();
-    // Rows that stay are the first ones (acc[k] = k only while every node so far is accepted).
-    if (threadIdx.x < n_acc) {
-        const int k = threadIdx.x, t0 = ctx + acc[k], t1 = ctx + k;
-        from_page[k] = *p.entry(b, t0 / p.page), from_row[k] = t0 % p.page;
-        to_page[k] = *p.entry(b, t1 / p.page), to_row[k] = t1 % p.page;
-        if (acc[k] != k) atomicAdd(&n_move, 1);
-    }
-    __syncthreads();
+__device__ __forceinline__ void move_rows(const PageRows &rows, const Moves &m, int k_first, int n_acc, int rank, int blocks) {
     const int cols = rows.row_bytes / (int)sizeof(V);
-    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (id >= (long long)units * cols) return;
-    const int unit = (int)(id / cols), c = (int)(id % cols);
+    const long long n = (long long)rows.n_layers * rows.pieces * cols;
     constexpr int U = 8;
-    for (int k0 = n_acc - n_move; k0 < n_acc; k0 += U) {
-        V v[U];
+    for (long long id = (long long)rank * blockDim.x + threadIdx.x; id < n; id += (long long)blocks * blockDim.x) {
+        const int unit = (int)(id / cols), c = (int)(id % cols);
+        for (int k0 = k_first; k0 < n_acc; k0 += U) {
+            V v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (k0 + u < n_acc)
-                v[u] = reinterpret_cast<const V *>(rows.at(unit, from_page[k0 + u]) + (size_t)from_row[k0 + u] * rows.row_bytes)[c];
+            for (int u = 0; u < U; ++u)
+                if (k0 + u < n_acc)
+                    v[u] = reinterpret_cast<const V *>(rows.at(unit, m.from_page[k0 + u]) +
+                                                       (size_t)m.from_row[k0 + u] * rows.row_bytes)[c];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (k0 + u < n_acc)
-                reinterpret_cast<V *>(rows.at(unit, to_page[k0 + u]) + (size_t)to_row[k0 + u] * rows.row_bytes)[c] = v[u];
+            for (int u = 0; u < U; ++u)
+                if (k0 + u < n_acc)
+                    reinterpret_cast<V *>(rows.at(unit, m.to_page[k0 + u]) + (size_t)m.to_row[k0 + u] * rows.row_bytes)[c] = v[u];
+        }
     }
 }
 
-__global__ void __launch_bounds__(64) accept_trim_kernel(Pool p, const int *__restrict__ ctx_lens,
-                                                         const int *__restrict__ n_nodes, const int *__restrict__ accepted,
-                                                         const int *__restrict__ n_accepted, int max_nodes) {
+// One cluster per request: moves the rows of every layer, then trims the request.
+constexpr int ACCEPT_THREADS = 288;   // 8 x 288 columns: the latent rows of 32 layers in one pass
+
+__global__ void __launch_bounds__(ACCEPT_THREADS, 4) accept_kernel(Pool p, const int *__restrict__ ctx_lens,
+                                                     const int *__restrict__ n_nodes, const int *__restrict__ accepted,
+                                                     const int *__restrict__ n_accepted, int max_nodes, RowSets sets) {
     step_begin();
-    const int b = blockIdx.x;
+    const int rank = blockIdx.x, blocks = gridDim.x, b = blockIdx.y;
     const int ctx = ctx_lens[b], n = n_nodes[b], n_acc = n_accepted[b];
-    if (!path_ok(p, b, ctx, n, accepted + (size_t)b * max_nodes, n_acc, max_nodes)) {
+    const int *acc = accepted + (size_t)b * max_nodes;
+    const bool ok = path_ok(p, b, ctx, n, acc, n_acc, max_nodes);
+    __shared__ Moves m;
+    __shared__ int n_move;
+    if (threadIdx.x == 0) n_move = 0;
+    __syncthreads();
+    if (ok) {
+        // Rows that stay are the first ones (acc[k] = k only while every node so far is accepted).
+        if (threadIdx.x < n_acc) {
+            const int k = threadIdx.x, t0 = ctx + acc[k], t1 = ctx + k;
+            m.from_page[k] = *p.entry(b, t0 / p.page), m.from_row[k] = t0 % p.page;
+            m.to_page[k] = *p.entry(b, t1 / p.page), m.to_row[k] = t1 % p.page;
+            if (acc[k] != k) atomicAdd(&n_move, 1);
+        }
+        __syncthreads();
+        if (n_move)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i >= sets.n) break;
+                const PageRows &r = sets.r[i];
+                if (r.vec == 16) move_rows<uint4>(r, m, n_acc - n_move, n_acc, rank, blocks);
+                else if (r.vec == 4) move_rows<uint32_t>(r, m, n_acc - n_move, n_acc, rank, blocks);
+                else move_rows<uint16_t>(r, m, n_acc - n_move, n_acc, rank, blocks);
+            }
+    }
+    cooperative_groups::this_cluster().sync();   // every block has read the page table
+    if (rank) return;
+    if (!ok) {
         if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
         return;
     }
@@ -391,23 +428,30 @@ Pool pool_of(const PagePool &a) {
     return Pool{a.seq_lens, a.page_table, a.refs, a.batch, a.max_pages, a.n_pages, a.page, a.err};
 }
 
-template <typename V>
-cudaError_t fork_copy(const Pool &p, const int *src, const int *dst, int n_fork, const PageRows &r, int units, int share,
-                      cudaStream_t st) {
-    const size_t piece = (size_t)p.page * (size_t)r.row_bytes;
-    dim3 grid(n_fork, r.base ? units : 1, r.base ? (unsigned)((piece + COPY_BYTES - 1) / COPY_BYTES) : 1);
-    MLA_STEP_LAUNCH(fork_copy_kernel<V>, grid, dim3(256), 0, st, p, src, dst, r, share);
-    return cudaGetLastError();
+// Launches one cluster of `blocks` blocks for each of `n` requests.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), int blocks, int threads, int n, cudaStream_t st, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, n);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = blocks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename V>
-cudaError_t accept_move(const Pool &p, const int *ctx, const int *n_nodes, const int *accepted, const int *n_accepted,
-                        int max_nodes, const PageRows &r, int units, cudaStream_t st) {
-    const long long threads = (long long)units * (r.row_bytes / (int)sizeof(V));
-    dim3 grid((unsigned)((threads + 127) / 128), p.batch);
-    MLA_STEP_LAUNCH(accept_move_kernel<V>, grid, dim3(128), 0, st, p, ctx, n_nodes, accepted, n_accepted, max_nodes, r,
-                    units);
-    return cudaGetLastError();
+RowSets sets_of(const PageRows *rows, int n) {
+    RowSets s{};
+    for (s.n = 0; s.n < n; ++s.n) s.r[s.n] = rows[s.n];
+    return s;
 }
 
 }  // namespace
@@ -421,17 +465,7 @@ cudaError_t launch_cache_fork(const PagePool &a, const int *src, const int *dst,
                               cudaStream_t st) {
     const Pool p = pool_of(a);
     MLA_STEP_LAUNCH(fork_plan_kernel, dim3(1), dim3(PT), 0, st, p, src, dst, n_fork);
-    cudaError_t e = n_rows ? cudaSuccess : fork_copy<uint4>(p, src, dst, n_fork, PageRows{}, 1, 1, st);
-    for (int i = 0; i < n_rows && e == cudaSuccess; ++i) {
-        const PageRows &r = rows[i];
-        const int units = r.n_layers * r.pieces;
-        e = r.vec == 16  ? fork_copy<uint4>(p, src, dst, n_fork, r, units, i == 0, st)
-            : r.vec == 4 ? fork_copy<uint32_t>(p, src, dst, n_fork, r, units, i == 0, st)
-                         : fork_copy<uint16_t>(p, src, dst, n_fork, r, units, i == 0, st);
-    }
-    if (e != cudaSuccess) return e;
-    MLA_STEP_LAUNCH(fork_finish_kernel, dim3(ceil_div(n_fork, 256)), dim3(256), 0, st, p, dst, n_fork);
-    return cudaGetLastError();
+    return launch_clusters(fork_copy_kernel, 8, 256, n_fork, st, p, src, dst, sets_of(rows, n_rows));
 }
 
 cudaError_t launch_cache_release(const PagePool &a, const int *req, const int *first, const int *last, int n_req,
@@ -442,18 +476,14 @@ cudaError_t launch_cache_release(const PagePool &a, const int *req, const int *f
 
 cudaError_t launch_cache_accept(const PagePool &a, const int *ctx, const int *n_nodes, const int *accepted,
                                 const int *n_accepted, int max_nodes, const PageRows *rows, int n_rows, cudaStream_t st) {
-    const Pool p = pool_of(a);
-    for (int i = 0; i < n_rows; ++i) {
-        const PageRows &r = rows[i];
-        const int units = r.n_layers * r.pieces;
-        const cudaError_t e =
-            r.vec == 16  ? accept_move<uint4>(p, ctx, n_nodes, accepted, n_accepted, max_nodes, r, units, st)
-            : r.vec == 4 ? accept_move<uint32_t>(p, ctx, n_nodes, accepted, n_accepted, max_nodes, r, units, st)
-                         : accept_move<uint16_t>(p, ctx, n_nodes, accepted, n_accepted, max_nodes, r, units, st);
-        if (e != cudaSuccess) return e;
-    }
-    MLA_STEP_LAUNCH(accept_trim_kernel, dim3(p.batch), dim3(64), 0, st, p, ctx, n_nodes, accepted, n_accepted, max_nodes);
-    return cudaGetLastError();
+    // Blocks enough for one pass over the columns of all rows, up to the portable cluster's eight.
+    long long cols = 1;
+    for (int i = 0; i < n_rows; ++i)
+        cols = std::max(cols, (long long)rows[i].n_layers * rows[i].pieces * (rows[i].row_bytes / rows[i].vec));
+    constexpr int T = ACCEPT_THREADS;
+    const int blocks = cols > 4 * T ? 8 : cols > 2 * T ? 4 : cols > T ? 2 : 1;
+    return launch_clusters(accept_kernel, blocks, T, a.batch, st, pool_of(a), ctx, n_nodes, accepted, n_accepted, max_nodes,
+                           sets_of(rows, n_rows));
 }
 
 }  // namespace mla

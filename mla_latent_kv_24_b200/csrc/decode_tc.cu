@@ -110,7 +110,9 @@ struct TcParams {
     const int *page_table;
     int max_pages, n_pages, s_q;
     float scale_log2;  // softmax scale * log2(e)
-    float *part_o;     // [n_work, 64, H, 8]: column octet-major (see the epilogue)
+    float *part_o;     // [n_work, 64, H, 8]: column octet-major (see the epilogue); with a view the
+                       // strides of an item's octets and heads say which of the two layouts
+    int oct_stride, head_stride;
     float *part_ml;    // [n_work, H, 2]: max (natural-log units), sum
     int *err;
     uint64_t wait_ns;  // limit of every barrier wait (WAIT_NS unless a test shortens it)
@@ -157,6 +159,10 @@ __device__ __forceinline__ int item_of_round(const Plan &pl, int pair, int n_pai
     return pl.order ? pl.order[j] : j;
 }
 
+// Out of line: inlined into every role, the mask's code made a step 0.1 us longer (the roles share the
+// SM's instruction cache).
+__device__ __noinline__ unsigned long long seen64_cold(const ItemView &iv, int t0) { return iv.seen64(t0); }
+
 // What an item sees.  Causal rows see all of [t0, t1); with VIEW the item's tokens are virtual and
 // only some of a page may be seen (view.cuh).
 template <bool VIEW>
@@ -165,12 +171,22 @@ struct Seen {
     __device__ __forceinline__ Seen(const TcParams &p, const WorkItem &it) {
         if (VIEW) iv = item_view(p.view, p.seq_lens, it.row / p.s_q, it.row % p.s_q, p.s_q, PAGE);
     }
+    // Whether the item sees all of the page at (virtual) token v0: two comparisons for nearly every
+    // page.  (Forming the 64-bit mask of every page in every role cost 0.5 us of a step's 1.9 us.)
+    __device__ __forceinline__ bool whole(const WorkItem &it, int v0) const {
+        return VIEW ? v0 >= iv.whole0 && v0 < iv.whole1 : v0 + PAGE <= it.t1;
+    }
     // Seen rows (bit = row) of the page that starts at (virtual) token v0.
     __device__ __forceinline__ unsigned long long page(const WorkItem &it, int v0) const {
+        if (whole(it, v0)) return ~0ull;
         const int n = it.t1 - v0;
         if (n <= 0) return 0ull;
-        if (VIEW) return iv.seen64(iv.token(v0));
-        return n >= PAGE ? ~0ull : (1ull << n) - 1ull;
+        return VIEW ? seen64_cold(iv, iv.token(v0)) : (1ull << n) - 1ull;
+    }
+    // Whether it sees a proper part of the page (the request's ragged last page, a window's first, a
+    // tree's nodes): the other rows may hold anything, NaN included.
+    __device__ __forceinline__ bool partly(const WorkItem &it, int v0) const {
+        return !whole(it, v0) && page(it, v0) != 0ull;
     }
     __device__ __forceinline__ int token(int v) const { return VIEW ? iv.token(v) : v; }
 };
@@ -180,7 +196,7 @@ struct Seen {
 // the end).
 template <bool VIEW>
 __device__ __forceinline__ int page_row(const TcParams &p, const Seen<VIEW> &sn, const WorkItem &it, int b, int v0) {
-    if (VIEW ? sn.page(it, v0) == 0ull : v0 >= it.t1) return p.n_pages * PAGE;
+    if (v0 >= it.t1 || (VIEW && sn.page(it, v0) == 0ull)) return p.n_pages * PAGE;
     const int pid = p.page_table[(size_t)b * p.max_pages + sn.token(v0) / PAGE];
     if (pid < 0 || pid >= p.n_pages) {
         report(p.err, MLA_ERR_DEVICE_BOUNDS);
@@ -228,10 +244,6 @@ __device__ void run_k_producer(const Ctx &c, const TcParams &p, const CUtensorMa
     }
 }
 
-// Whether an item sees a proper part of a page (the request's ragged last page, a window's first, a
-// tree's nodes): the other rows may hold anything, NaN included.
-__device__ __forceinline__ bool partly(unsigned long long seen) { return seen != 0ull && seen != ~0ull; }
-
 // V producer (lane 0): per step and page pg of the step, this CTA's 256 latent columns of that
 // page.  A partly seen page is copied with this CTA's own barrier instead, and its unseen rows are
 // cleared by run_v_tail.
@@ -249,7 +261,7 @@ __device__ void run_v_producer(const Ctx &c, const TcParams &p, const CUtensorMa
             for (int pg = 0; pg < NV; ++pg) {
                 const int y = page_row(p, sn, it, b, t_step + PAGE * pg);
                 if (!wait_or_abort(c, c.bar(B_VEMPTY + pg), ((uint32_t)g & 1u) ^ 1u, p.err)) return;
-                if (!partly(sn.page(it, t_step + PAGE * pg))) {
+                if (!sn.partly(it, t_step + PAGE * pg)) {
                     if (c.rank == 0) tc::mbar_arrive_expect_tx(c.bar(B_VFULL + pg), 2u * VSLOT);
                     tc::tma_load_4d_pair(c.vslot(pg), tm_v, 0, y, 2 * (int)c.rank, 0, c.lead_bar(B_VFULL + pg));
                 } else {
@@ -278,8 +290,8 @@ __device__ void run_v_tail(const Ctx &c, const TcParams &p, int pair, int n_pair
         const Seen<VIEW> sn(p, it);
         for (int i = VIEW ? 0 : n_steps - 1; i < n_steps; ++i)   // a causal row's end is in its last step
             for (int pg = 0; pg < NV; ++pg) {
+                if (!sn.partly(it, it.t0 + STEP * i + PAGE * pg)) continue;
                 const unsigned long long seen = sn.page(it, it.t0 + STEP * i + PAGE * pg);
-                if (!partly(seen)) continue;
                 const bool ok = wait_or_abort(c, c.bar(B_VLOCAL + pg), (ph >> pg) & 1u, p.err);
                 ph ^= 1u << pg;
                 if (!__all_sync(0xfffffffeu, ok)) return;
@@ -368,7 +380,7 @@ __device__ void run_pv_issuer(const Ctx &c, const TcParams &p, uint32_t tmem, in
 #pragma unroll
             for (int pg = 0; pg < NV; ++pg) {
                 if (!wait_or_abort<true>(c, c.bar(B_VFULL + pg), (uint32_t)g & 1u, p.err)) return;
-                if (partly(sn.page(it, it.t0 + STEP * i + PAGE * pg))) {
+                if (sn.partly(it, it.t0 + STEP * i + PAGE * pg)) {
                     if (!wait_or_abort<true>(c, c.bar(B_VTAIL + pg), (ph >> pg) & 1u, p.err)) return;
                     ph ^= 1u << pg;
                 }
@@ -443,11 +455,17 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
 
             const int tok0 = it.t0 + STEP * i + 64 * hsel + 32 * half;
             const int nvalid = min(32, max(0, it.t1 - tok0));
-            const uint32_t seen = VIEW ? (uint32_t)(sn.page(it, tok0 - 32 * half) >> (32 * half)) : 0u;
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (VIEW) {
+                if (!sn.whole(it, tok0 - 32 * half)) {   // the same for the whole warp
+                    const uint32_t seen = (uint32_t)(sn.page(it, tok0 - 32 * half) >> (32 * half));
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[j] = (seen >> j) & 1u ? s[j] : -INFINITY;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                s[j] = (VIEW ? (seen >> j) & 1u : j < nvalid) ? s[j] : -INFINITY;
+                if (!VIEW) s[j] = j < nvalid ? s[j] : -INFINITY;
                 m4[j & 3] = fmaxf(m4[j & 3], s[j]);
             }
             float o1, o2, o3;
@@ -543,7 +561,11 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
 #pragma unroll
             for (int jo = 0; jo < 8; ++jo) {
                 const int oct = 32 * half + 16 * hsel + 8 * q + jo;
-                tc::st_global_v8(p.part_o + (((size_t)k * 64 + oct) * H + head) * 8, v + 8 * jo);
+                if (VIEW)   // either layout, for the kernel that merges
+                    tc::st_global_v8(p.part_o + (size_t)k * 64 * H * 8 + (uint32_t)(oct * p.oct_stride + head * p.head_stride),
+                                     v + 8 * jo);
+                else
+                    tc::st_global_v8(p.part_o + (((size_t)k * 64 + oct) * H + head) * 8, v + 8 * jo);
             }
         }
         tc::fence_before_sync();
@@ -744,7 +766,7 @@ int tc_token_granule() { return STEP; }
 
 cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *latent, const int *page_table,
                              const Plan &plan, int max_pages, int n_pages, int s_q, float *part_o, float *part_ml,
-                             int *err, int sms, cudaStream_t st, const View &view, const int *seq_lens) {
+                             int *err, int sms, cudaStream_t st, const View &view, const int *seq_lens, bool oct_layout) {
     if (plan.n_work == 0) return cudaSuccess;
     CUtensorMap tm_q, tm_k, tm_v;
     const uint64_t kv_rows = (uint64_t)n_pages * PAGE;
@@ -765,6 +787,8 @@ cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *laten
     p.withhold = g_test_withhold;
     p.view = view;
     p.seq_lens = seq_lens;
+    p.oct_stride = oct_layout ? 8 * H : 8;
+    p.head_stride = oct_layout ? 8 : 512;
     auto k = view.kind == VIEW_CAUSAL ? tc_decode_kernel<false> : tc_decode_kernel<true>;
     cudaError_t e = raise_smem_limit((const void *)k, SMEM_ALLOC);
     if (e != cudaSuccess) return e;

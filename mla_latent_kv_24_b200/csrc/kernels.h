@@ -81,15 +81,18 @@ cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part
 // rows_host: the plan's row starts computed on the host from the host lengths (rows + 1 values),
 // or nullptr; batches of at most RowStarts::MAX rows pass them by value, which saves the kernel a
 // dependent load (the device plan still validates the lengths and reports a mismatch).
+// fine: the merged latent rows enter the product as two bf16 values each (16 bits of their value)
+// instead of one.  With combine_by_head(rows) such a call needs the [n_work, H, 512] layout.
 struct RowStarts {
     static constexpr int MAX = 64;
     int n;              // rows covered (0: read row_first from the workspace)
     int v[MAX + 1];
 };
+bool combine_by_head(int rows);
 bool combine_mma_ok(const Dims &d, int DV, bool project);
 cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *part_ml, const int *row_first,
                                const int *rows_host, int rows, bool oct_layout, const void *W_uv, void *out,
-                               cudaStream_t st, bool keep_empty = false);
+                               cudaStream_t st, bool keep_empty = false, bool fine = false);
 
 // Per-group cache expansion (expand.cu).
 cudaError_t launch_expand(const Dims &d, const void *W_uk, const void *W_uv, const void *latent,

@@ -13,7 +13,8 @@ int tc_token_granule();       // chunk lengths are multiples of this many tokens
 cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *latent, const int *page_table,
                              const Plan &plan, int max_pages, int n_pages, int s_q, float *part_o,
                              float *part_ml, int *err, int sms, cudaStream_t st, const View &view = View{},
-                             const int *seq_lens = nullptr);   // seq_lens: for the views other than causal
+                             const int *seq_lens = nullptr,    // for the views other than causal
+                             bool oct_layout = true);          // false: partials [n_work, H, 512]
 
 // Test hook of the bounded waits: later tcgen05 decodes on the calling thread skip the completion
 // signal of pipeline step `withhold_step` (-1: none) and give up every wait after `wait_ns`
@@ -22,7 +23,7 @@ void tc_set_test_fault(int withhold_step, uint64_t wait_ns);
 
 // Grouped path, bf16, d_nope = d_v = 128, d_rope = 64, heads_per_group = 8.
 bool grouped_tc_ok(const Dims &d, int s_q);   // s_q <= 4: 16-row tiles of 8 heads x 2 queries
-int grouped_units(const Dims &d, int sms);
+int grouped_units(const Dims &d, int sms, bool window = false);
 int grouped_token_granule();
 // Head-expanded prefill over the expanded cache (per head with heads_per_group = 1, or per
 // group): bf16, d_nope = d_v = 128, d_rope = 64, d_c = 512, page 64.  n_q query tokens per

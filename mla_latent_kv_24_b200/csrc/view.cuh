@@ -70,6 +70,7 @@ struct ItemView {
     unsigned long long mask;         // tree: bit i = token ctx + i
     int ctx;
     bool tree;
+    int whole0, whole1;              // virtual tokens [whole0, whole1) are all seen; multiples of 64
 
     MLA_HD int token(int v) const { return v < span.gap_at ? v : v + span.gap; }
 
@@ -108,6 +109,8 @@ MLA_HD ItemView item_view(const View &v, const int *seq_lens, int b, int j, int 
         iv.mask = v.mask[(size_t)b * n_q + j];
         if (n < 64) iv.mask &= (1ull << n) - 1ull;
         iv.lo = 0, iv.sinks = 0, iv.end = L;
+        iv.whole0 = 0;
+        iv.whole1 = iv.ctx / 64 * 64;
     } else {
         const int p0 = j < 0 ? L - n_q : L - n_q + j, p1 = j < 0 ? L - 1 : p0;
         iv.span = window_span(v.sinks, v.window, p0, p1, page);
@@ -115,6 +118,9 @@ MLA_HD ItemView item_view(const View &v, const int *seq_lens, int b, int j, int 
         iv.sinks = v.sinks;
         iv.end = p1 + 1;
         iv.ctx = 0, iv.mask = 0;
+        // The window's whole pages; the sinks' pages are few.  (Pages other than 64 tokens: not used.)
+        iv.whole0 = (iv.lo + 63) / 64 * 64 - iv.span.gap;
+        iv.whole1 = iv.end / 64 * 64 - iv.span.gap;
     }
     return iv;
 }
