@@ -11,18 +11,12 @@
 // rows; every thread owns two latent columns.
 #include "kernels.h"
 #include "plan_block.cuh"
+#include "rope_rows.cuh"
 
 namespace mla {
 namespace {
 
 constexpr int RB = 16;
-
-// Position of query j of request b: the s_q queries are the request's last tokens, and a tree's
-// node sits at its depth behind the context.
-__device__ __forceinline__ int query_pos(const View &v, const int *seq_lens, int b, int j, int s_q) {
-    if (v.kind == VIEW_TREE) return seq_lens[b] - v.n_nodes[b] + v.depths[(size_t)b * s_q + j];
-    return seq_lens[b] - s_q + j;
-}
 
 template <typename T>
 __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, const T *__restrict__ W_uk,
@@ -174,42 +168,6 @@ namespace {
 
 constexpr int AB_K = 128, AB_LD = AB_K + 8, AB_N = 128, AB_LDB = AB_N + 8;
 constexpr int D_C = 512, D_N = 128, D_R = 64, D_QK = 192, D_OUT = 576;
-constexpr int ROPE_WARPS = 8;   // warps of a row: each takes every eighth head
-
-// Blocks past the heads' (see above); `id` counts them.
-__device__ __forceinline__ void absorb_extra_block(int id, const __nv_bfloat16 *__restrict__ q,
-                                                   const int *__restrict__ seq_lens, int rows, int s_q, int H, float base,
-                                                   __nv_bfloat16 *__restrict__ q_abs, const PlanArgs &plan, int *scratch,
-                                                   int cap) {
-    if (id == 0) {
-        plan_block<256>(plan, scratch, cap);
-        return;
-    }
-    const int row = id - 1, lane = threadIdx.x % 32, first = threadIdx.x / 32;
-    if (row >= rows) {
-        step_wait_prev();
-        return;
-    }
-    constexpr int U = 16;
-    const int b = row / s_q, j = row % s_q;
-    const __nv_bfloat16 *src = q + (size_t)row * H * D_QK + D_N + 2 * lane;
-    __nv_bfloat16 *dst = q_abs + (size_t)row * H * D_OUT + D_C + 2 * lane;
-    uint32_t x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = first + ROPE_WARPS * u;
-        x[u] = h < H ? *reinterpret_cast<const uint32_t *>(src + (size_t)h * D_QK) : 0u;
-    }
-    float cs, sn;
-    rope_cos_sin(query_pos(plan.view, seq_lens, b, j, s_q), lane, D_R, base, &cs, &sn);
-    step_wait_prev();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {   // H <= 128 = U ROPE_WARPS
-        const int h = first + ROPE_WARPS * u;
-        const float x0 = __uint_as_float(x[u] << 16), x1 = __uint_as_float(x[u] & 0xffff0000u);
-        if (h < H) *reinterpret_cast<uint32_t *>(dst + (size_t)h * D_OUT) = pack_bf16(x0 * cs - x1 * sn, x0 * sn + x1 * cs);
-    }
-}
 
 // One warp's 16 x (8 NT) product of the staged tiles.
 template <int NT>
@@ -261,7 +219,7 @@ __global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *
     __shared__ __align__(16) __nv_bfloat16 Bs[AB_K * AB_LDB];       // [128 k][128 n]
     const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
     if (h >= H) {
-        absorb_extra_block((h - H) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base, q_abs, plan,
+        rope_or_plan_block((h - H) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base, q_abs, plan,
                            reinterpret_cast<int *>(Bs), ((int)sizeof(Bs) / 4 - 1) / 2);
         return;
     }
@@ -301,7 +259,7 @@ __global__ void __launch_bounds__(256, 3) q_absorb_rows_kernel(const __nv_bfloat
     __nv_bfloat16 *As = Bs + AB_K * AB_LDB;                         // [2][64 rows][128 k]; a tile's output too
     const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
     if (h >= H) {
-        absorb_extra_block(((h - H) * gridDim.z + blockIdx.z) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base,
+        rope_or_plan_block(((h - H) * gridDim.z + blockIdx.z) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base,
                            q_abs, plan, reinterpret_cast<int *>(Bs), (AB_K * AB_LDB / 2 - 1) / 2);
         return;
     }
@@ -351,7 +309,7 @@ cudaError_t launch_q_absorb_mma(const Dims &d, const void *q, const void *W_uk, 
     const int rows = batch * s_q;
     constexpr int Y = D_C / AB_N;
     if (rows <= 16) {
-        dim3 grid(d.H + ceil_div(1 + rows, Y), Y, 1);
+        dim3 grid(d.H + ceil_div(1 + rope_blocks(rows), Y), Y, 1);
         MLA_STEP_LAUNCH(q_absorb_mma_kernel, grid, dim3(256), 0, st, (const __nv_bfloat16 *)q,
                         (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs,
                         plan);
@@ -359,7 +317,7 @@ cudaError_t launch_q_absorb_mma(const Dims &d, const void *q, const void *W_uk, 
         // Two tiles per CTA: enough to hide the queries' loads, short enough to share the SMs evenly.
         const int z = std::min(ceil_div(ceil_div(rows, ABR), 2), 65535);
         const long long per = (long long)Y * z;
-        dim3 grid(d.H + (unsigned)((rows + per) / per), Y, z);   // + blocks for the plan and `rows` RoPE rows
+        dim3 grid(d.H + (unsigned)((rope_blocks(rows) + per) / per), Y, z);   // + the plan's and the RoPE blocks
         cudaError_t e = raise_smem_limit((const void *)q_absorb_rows_kernel, AB_ROWS_SMEM);
         if (e != cudaSuccess) return e;
         MLA_STEP_LAUNCH(q_absorb_rows_kernel, grid, dim3(256), AB_ROWS_SMEM, st, (const __nv_bfloat16 *)q,

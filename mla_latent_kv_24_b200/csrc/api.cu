@@ -408,7 +408,9 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                       hv.v, s_q};
     const bool keep_empty = hv.v.kind == VIEW_TREE;   // node slots past a request's count keep their output
     if (path == ABSORBED) {
-        if (q_absorb_mma_ok(d)) {
+        if (tc && hv.v.kind != VIEW_CAUSAL && absorb_tc_pays(L.rows)) {
+            MLA_CUDA(launch_absorb_tc(d, q, W_uk, seq_lens, batch, s_q, qp, pa, st), "launch q_absorb (tcgen05) + plan");
+        } else if (q_absorb_mma_ok(d)) {
             MLA_CUDA(launch_q_absorb_mma(d, q, W_uk, seq_lens, batch, s_q, qp, pa, st),
                      "launch q_absorb (tensor cores) + plan");
         } else {
@@ -428,7 +430,10 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                              hv.v, seq_lens};
             MLA_CUDA(launch_decode_simt(d, a, st), "launch decode (CUDA cores)");
         }
-        if (combine_mma_ok(d, L.DV, true)) {
+        if (tc && !oct && project_tc_pays(L.rows)) {
+            MLA_CUDA(launch_project_tc(d, part_o, part_ml, row_first, L.rows, W_uv, out, err, st, keep_empty),
+                     "launch merge + W_UV (tcgen05)");
+        } else if (combine_mma_ok(d, L.DV, true)) {
             // The plan's row starts from the host lengths (the device plan is built from the same rule).
             int starts[RowStarts::MAX + 1];
             const int *sp = nullptr;

@@ -386,13 +386,14 @@ __global__ void __launch_bounds__(256) project_rows_kernel(const float *__restri
     const float2 *ml = reinterpret_cast<const float2 *>(part_ml);
     float2 first = make_float2(-INFINITY, 0.f);
     if (k0 < k1) first = ml[(size_t)k0 * H + h];
-    auto chunk = [&](int k, int s) {   // this thread's float4s of chunk k, slice s: sub, sub + TPR, ...
-        return reinterpret_cast<const float4 *>(part_o + ((size_t)k * H + h) * CK + s * XC) + sub;
+    auto at4 = [&](int k, int s, int i) {   // this thread's i-th float4 of chunk k, slice s
+        const int c = sub + i * TPR;          // 0..31: two blocks of 64 columns
+        return reinterpret_cast<const float4 *>(part_o + (((size_t)k * 8 + 2 * s + c / 16) * H + h) * 64) + c % 16;
     };
     float4 x[F4];
     auto load_first = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < F4; ++i) x[i] = k0 < k1 ? __ldcs(chunk(k0, s) + i * TPR) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < F4; ++i) x[i] = k0 < k1 ? __ldcs(at4(k0, s, i)) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load_first(0);
     float M = first.x, den = first.y;
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(256) project_rows_kernel(const float *__restri
             const float wk = mk == -INFINITY ? 0.f : expf(mk - M) * inv;
 #pragma unroll
             for (int i = 0; i < F4; ++i) {
-                const float4 v = __ldcs(chunk(k, s) + i * TPR);
+                const float4 v = __ldcs(at4(k, s, i));
                 x[i].x += wk * v.x, x[i].y += wk * v.y, x[i].z += wk * v.z, x[i].w += wk * v.w;
             }
         }

@@ -110,8 +110,8 @@ struct TcParams {
     const int *page_table;
     int max_pages, n_pages, s_q;
     float scale_log2;  // softmax scale * log2(e)
-    float *part_o;     // [n_work, 64, H, 8]: column octet-major (see the epilogue); with a view the
-                       // strides of an item's octets and heads say which of the two layouts
+    float *part_o;     // [n_work, 64, H, 8]: column octet-major (see the epilogue); with a view, by the
+                       // strides of an octet and a head inside 64 columns, that or [n_work, 8, H, 64]
     int oct_stride, head_stride;
     float *part_ml;    // [n_work, H, 2]: max (natural-log units), sum
     int *err;
@@ -562,7 +562,8 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
             for (int jo = 0; jo < 8; ++jo) {
                 const int oct = 32 * half + 16 * hsel + 8 * q + jo;
                 if (VIEW)   // either layout, for the kernel that merges
-                    tc::st_global_v8(p.part_o + (size_t)k * 64 * H * 8 + (uint32_t)(oct * p.oct_stride + head * p.head_stride),
+                    tc::st_global_v8(p.part_o + (size_t)k * 64 * H * 8 + (oct / 8) * 64 * H +
+                                         (uint32_t)(jo * p.oct_stride + head * p.head_stride),
                                      v + 8 * jo);
                 else
                     tc::st_global_v8(p.part_o + (((size_t)k * 64 + oct) * H + head) * 8, v + 8 * jo);
@@ -788,7 +789,7 @@ cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *laten
     p.view = view;
     p.seq_lens = seq_lens;
     p.oct_stride = oct_layout ? 8 * H : 8;
-    p.head_stride = oct_layout ? 8 : 512;
+    p.head_stride = oct_layout ? 8 : 64;
     auto k = view.kind == VIEW_CAUSAL ? tc_decode_kernel<false> : tc_decode_kernel<true>;
     cudaError_t e = raise_smem_limit((const void *)k, SMEM_ALLOC);
     if (e != cudaSuccess) return e;
