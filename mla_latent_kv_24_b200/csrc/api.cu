@@ -418,11 +418,13 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
             MLA_CUDA(launch_q_absorb(d, q, W_uk, seq_lens, batch, s_q, qp, st, hv.v), "launch q_absorb");
         }
         // A view's rows are merged by the kernel that suits their number, each from its own layout.
-        const bool oct = tc && (hv.v.kind == VIEW_CAUSAL || !combine_by_head(L.rows));
+        const PartLayout parts = !tc                                                             ? PART_ROWS
+                                 : hv.v.kind != VIEW_CAUSAL && combine_by_head(L.rows) ? PART_BLOCKS
+                                                                                       : PART_OCTETS;
         if (tc) {
             ProfileScope prof(st);
             MLA_CUDA(launch_tc_decode(d, qp, latent, page_table, plan, max_pages, n_pages, s_q, part_o, part_ml, err, sms,
-                                      st, hv.v, seq_lens, oct),
+                                      st, hv.v, seq_lens, parts),
                      "launch tcgen05 decode");
         } else {
             ProfileScope prof(st);
@@ -430,7 +432,7 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                              hv.v, seq_lens};
             MLA_CUDA(launch_decode_simt(d, a, st), "launch decode (CUDA cores)");
         }
-        if (tc && !oct && project_tc_pays(L.rows)) {
+        if (parts == PART_BLOCKS && project_tc_pays(L.rows)) {
             MLA_CUDA(launch_project_tc(d, part_o, part_ml, row_first, L.rows, W_uv, out, err, st, keep_empty),
                      "launch merge + W_UV (tcgen05)");
         } else if (combine_mma_ok(d, L.DV, true)) {
@@ -445,12 +447,14 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                 }
                 if (starts[L.rows] == L.n_work) sp = starts;
             }
-            MLA_CUDA(launch_combine_mma(d, part_o, part_ml, row_first, sp, L.rows, oct, W_uv, out, st,
+            MLA_CUDA(launch_combine_mma(d, part_o, part_ml, row_first, sp, L.rows, parts, W_uv, out, st,
                                         keep_empty, hv.v.kind != VIEW_CAUSAL),
                      "launch combine + W_UV (tensor cores)");
         }
         else if (!tc)
-            MLA_CUDA(launch_combine(d, part_o, part_ml, row_first, L.rows, 1, L.DV, W_uv, out, st, keep_empty),
+            MLA_CUDA(hv.v.kind == VIEW_CAUSAL
+                         ? launch_combine(d, part_o, part_ml, row_first, L.rows, 1, L.DV, W_uv, out, st)
+                         : launch_combine_view(d, part_o, part_ml, row_first, L.rows, L.DV, W_uv, out, st, keep_empty),
                      "launch combine");
         else
             return fail(MLA_ERR_UNSUPPORTED, "tcgen05 partials need the tensor-core combine");

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
                                                       const float *__restrict__ part_ml,
                                                       const int *__restrict__ row_first, int rows, int qpi,
                                                       int H, int DV, const T *__restrict__ W_uv, int hpw,
-                                                      int d_v, T *__restrict__ out, bool keep_empty) {
+                                                      int d_v, T *__restrict__ out) {
     step_begin();
     extern __shared__ float O[];  // [RB][DV]
     const int h = blockIdx.x;
@@ -52,14 +52,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
         }
     }
     __syncthreads();
-    auto kept = [&](int r) {   // row row0 + r has no work items and keeps what it holds
-        const int pr = (row0 + r) / qpi;
-        return keep_empty && row_first[pr] == row_first[pr + 1];
-    };
     if (W_uv == nullptr) {
         for (int i = threadIdx.x; i < nr * DV; i += blockDim.x) {
             const int r = i / DV, c = i % DV;
-            if (!kept(r)) out[((size_t)(row0 + r) * H + h) * DV + c] = from_f32<T>(O[r * DV + c]);
+            out[((size_t)(row0 + r) * H + h) * DV + c] = from_f32<T>(O[r * DV + c]);
         }
         return;
     }
@@ -74,8 +70,71 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
 #pragma unroll
             for (int r = 0; r < RB; ++r) acc[r] += wv * O[r * DV + k];
         }
-        for (int r = 0; r < nr; ++r)
-            if (!kept(r)) out[((size_t)(row0 + r) * H + h) * d_v + v] = from_f32<T>(acc[r]);
+        for (int r = 0; r < nr; ++r) out[((size_t)(row0 + r) * H + h) * d_v + v] = from_f32<T>(acc[r]);
+    }
+}
+
+// Merge + W_UV for the views' general shapes: combine_kernel with a warp per row, whose lanes share the
+// chunks of the maximum and the sum, instead of one row after another (64 rows of 11 chunks at the tiny
+// float32 shape: 42 -> PLACEHOLDER us).  keep_empty: rows without work items keep what `out` holds.
+template <typename T>
+__global__ void __launch_bounds__(32 * RB) combine_view_kernel(const float *__restrict__ part_o,
+                                                               const float *__restrict__ part_ml,
+                                                               const int *__restrict__ row_first, int rows, int H, int DV,
+                                                               const T *__restrict__ W_uv, int hpw, int d_v,
+                                                               T *__restrict__ out, bool keep_empty) {
+    step_begin();
+    extern __shared__ float O[];   // [RB][DV]
+    __shared__ int kept[RB];
+    const int h = blockIdx.x, row0 = blockIdx.y * RB, nr = min(RB, rows - row0);
+    const int r = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (r < nr) {
+        const int k0 = row_first[row0 + r], k1 = row_first[row0 + r + 1];
+        if (lane == 0) kept[r] = keep_empty && k0 == k1;
+        float M = -INFINITY;
+        for (int k = k0 + lane; k < k1; k += 32) M = fmaxf(M, part_ml[((size_t)k * H + h) * 2]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int c0 = 0; c0 < DV; c0 += 128) {   // four columns a lane
+            float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+            for (int kb = k0; kb < k1; kb += 32) {
+                float w = 0.f;
+                if (kb + lane < k1) {
+                    const float2 ml = reinterpret_cast<const float2 *>(part_ml)[(size_t)(kb + lane) * H + h];
+                    if (ml.x != -INFINITY) {
+                        w = expf(ml.x - M);
+                        den += w * ml.y;
+                    }
+                }
+                const int n = min(32, k1 - kb);
+#pragma unroll 4
+                for (int u = 0; u < n; ++u) {
+                    const float wu = __shfl_sync(0xffffffffu, w, u);
+                    const float *p = part_o + ((size_t)(kb + u) * H + h) * DV + c0 + lane;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c0 + lane + 32 * e < DV) num[e] += wu * p[32 * e];
+                }
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+            const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c0 + lane + 32 * e < DV) O[r * DV + c0 + lane + 32 * e] = num[e] * inv;
+        }
+    }
+    __syncthreads();
+    const T *W = W_uv + (size_t)(h / hpw) * d_v * DV;
+    for (int i = threadIdx.x; i < nr * d_v; i += blockDim.x) {
+        const int rr = i / d_v, v = i % d_v;
+        if (kept[rr]) continue;
+        const T *wr = W + (size_t)v * DV;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};   // d_c is a multiple of 8
+        for (int k = 0; k < DV; k += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += to_f32(wr[k + e]) * O[rr * DV + k + e];
+        out[((size_t)(row0 + rr) * H + h) * d_v + v] = from_f32<T>((acc[0] + acc[1]) + (acc[2] + acc[3]));
     }
 }
 
@@ -87,7 +146,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) combine_rows_kernel(const float *__restrict__ part_o,
                                                            const float *__restrict__ part_ml,
                                                            const int *__restrict__ row_first, int rows, int qpi,
-                                                           int H, int DV, T *__restrict__ out, bool keep_empty) {
+                                                           int H, int DV, T *__restrict__ out) {
     step_begin();
     const int lane = threadIdx.x % 32;
     const long long wid = (long long)blockIdx.x * 8 + threadIdx.x / 32;
@@ -95,7 +154,6 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const float *__restri
     const int row = (int)(wid / H), h = (int)(wid % H);
     const int pr = row / qpi, j = row % qpi;
     const int k0 = row_first[pr], k1 = row_first[pr + 1];
-    if (keep_empty && k0 == k1) return;
     auto idx = [&](int k) { return ((size_t)k * qpi + j) * H + h; };
     float M = -INFINITY;
     for (int k = k0 + lane; k < k1; k += 32) M = fmaxf(M, part_ml[idx(k) * 2]);
@@ -144,17 +202,17 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const float *__restri
 }  // namespace
 
 cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part_ml, const int *row_first,
-                           int rows, int qpi, int DV, const void *W_uv, void *out, cudaStream_t st, bool keep_empty) {
+                           int rows, int qpi, int DV, const void *W_uv, void *out, cudaStream_t st) {
     if (W_uv == nullptr && DV % 4 == 0) {
         const long long warps = (long long)rows * d.H;
         if (warps == 0) return cudaSuccess;
         const unsigned blocks = (unsigned)((warps + 7) / 8);
         if (d.bf16)
             MLA_STEP_LAUNCH(combine_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, st, part_o, part_ml,
-                            row_first, rows, qpi, d.H, DV, (__nv_bfloat16 *)out, keep_empty);
+                            row_first, rows, qpi, d.H, DV, (__nv_bfloat16 *)out);
         else
             MLA_STEP_LAUNCH(combine_rows_kernel<float>, dim3(blocks), dim3(256), 0, st, part_o, part_ml, row_first,
-                            rows, qpi, d.H, DV, (float *)out, keep_empty);
+                            rows, qpi, d.H, DV, (float *)out);
         return cudaGetLastError();
     }
     dim3 grid(d.H, ceil_div(rows, RB));
@@ -164,14 +222,28 @@ cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part
         cudaError_t e = raise_smem_limit((const void *)k, smem);
         if (e != cudaSuccess) return e;
         MLA_STEP_LAUNCH(k, dim3(grid), dim3(256), smem, st, part_o, part_ml, row_first, rows, qpi, d.H, DV,
-                        (const __nv_bfloat16 *)W_uv, d.hpw, d.d_v, (__nv_bfloat16 *)out, keep_empty);
+                        (const __nv_bfloat16 *)W_uv, d.hpw, d.d_v, (__nv_bfloat16 *)out);
     } else {
         auto k = combine_kernel<float>;
         cudaError_t e = raise_smem_limit((const void *)k, smem);
         if (e != cudaSuccess) return e;
         MLA_STEP_LAUNCH(k, dim3(grid), dim3(256), smem, st, part_o, part_ml, row_first, rows, qpi, d.H, DV,
-                        (const float *)W_uv, d.hpw, d.d_v, (float *)out, keep_empty);
+                        (const float *)W_uv, d.hpw, d.d_v, (float *)out);
     }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_view(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
+                                int DV, const void *W_uv, void *out, cudaStream_t st, bool keep_empty) {
+    if (ceil_div(rows, RB) > 65535) return cudaErrorInvalidValue;
+    const dim3 grid(d.H, ceil_div(rows, RB));
+    const size_t smem = sizeof(float) * RB * DV;   // at most 16 KiB
+    if (d.bf16)
+        MLA_STEP_LAUNCH(combine_view_kernel<__nv_bfloat16>, grid, dim3(32 * RB), smem, st, part_o, part_ml, row_first, rows,
+                        d.H, DV, (const __nv_bfloat16 *)W_uv, d.hpw, d.d_v, (__nv_bfloat16 *)out, keep_empty);
+    else
+        MLA_STEP_LAUNCH(combine_view_kernel<float>, grid, dim3(32 * RB), smem, st, part_o, part_ml, row_first, rows, d.H, DV,
+                        (const float *)W_uv, d.hpw, d.d_v, (float *)out, keep_empty);
     return cudaGetLastError();
 }
 
@@ -341,9 +413,8 @@ __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
 // Merge + W_UV for the trees' and windows' decodes, whose batches have up to thousands of rows.
 //
 // One CTA takes a head and PM rows and walks the latent in four slices of 128 columns.  Per slice it
-// merges the rows' chunk partials ([item][H][512] fp32: a head's slice of a row is 512 contiguous
-// bytes; a row with one chunk, the usual case, is only scaled by 1 / l), splits each merged value x
-// into two bf16 values hi = bf16(x), lo = bf16(x - hi), and adds (hi + lo) W_UV[w][:, slice]^T with
+// merges the rows' chunk partials ([item][8][H][64] fp32; a row with one chunk, the usual case, is only
+// scaled by 1 / l), splits each merged value x into two bf16 values hi = bf16(x), lo = bf16(x - hi), and adds (hi + lo) W_UV[w][:, slice]^T with
 // mma.sync m16n8k16: the merged latent keeps 16 bits of its value, so that the product adds no
 // rounding of its own to the output's (with hi alone the outputs were 0.0030 off in relative norm
 // instead of 0.0025).  The next slice's partials are in flight in registers and its W_UV tile by
@@ -497,7 +568,8 @@ cudaError_t launch_project(const Dims &d, const float *part_o, const float *part
 
 }  // namespace
 
-// Rows from which project_rows_kernel merges a view's partials instead of the cluster kernel.
+// One 16-row tile in the cluster kernel, from octets; more rows by head (8 rows: 31.7 us a call in clusters,
+// 49.8 by head; 16: 36.0 and 41.6; 32: 48.9 and 44.7).
 bool combine_by_head(int rows) { return rows > CM_FINE; }
 
 bool combine_mma_ok(const Dims &d, int DV, bool project) {
@@ -505,10 +577,10 @@ bool combine_mma_ok(const Dims &d, int DV, bool project) {
 }
 
 cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *part_ml, const int *row_first,
-                               const int *rows_host, int rows, bool oct_layout, const void *W_uv, void *out,
+                               const int *rows_host, int rows, PartLayout layout, const void *W_uv, void *out,
                                cudaStream_t st, bool keep_empty, bool fine) {
     if (rows <= 0) return cudaSuccess;
-    if (fine && combine_by_head(rows))
+    if (layout == PART_BLOCKS)
         return launch_project<64>(d, part_o, part_ml, row_first, rows, W_uv, out, st, keep_empty);
     RowStarts rs;
     rs.n = 0;
@@ -523,7 +595,8 @@ cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *
     const int cm = fine ? CM_FINE : CM_ROWS;
     if (ceil_div(rows, cm) > 65535 || d.H > 65535) return cudaErrorInvalidValue;
     dim3 grid(XS, d.H, ceil_div(rows, cm));
-    auto k = oct_layout ? (fine ? combine_split_kernel<true, true, CM_FINE> : combine_split_kernel<true, false, CM_ROWS>)
+    auto k = layout == PART_OCTETS
+                        ? (fine ? combine_split_kernel<true, true, CM_FINE> : combine_split_kernel<true, false, CM_ROWS>)
                         : (fine ? combine_split_kernel<false, true, CM_FINE> : combine_split_kernel<false, false, CM_ROWS>);
     cudaError_t e = raise_smem_limit((const void *)k, smem);
     if (e != cudaSuccess) return e;

@@ -186,7 +186,9 @@ struct Seen {
     // Whether it sees a proper part of the page (the request's ragged last page, a window's first, a
     // tree's nodes): the other rows may hold anything, NaN included.
     __device__ __forceinline__ bool partly(const WorkItem &it, int v0) const {
-        return !whole(it, v0) && page(it, v0) != 0ull;
+        if (whole(it, v0)) return false;
+        const unsigned long long m = page(it, v0);
+        return m != 0ull && m != ~0ull;
     }
     __device__ __forceinline__ int token(int v) const { return VIEW ? iv.token(v) : v; }
 };
@@ -304,9 +306,12 @@ __device__ void run_v_tail(const Ctx &c, const TcParams &p, int pair, int n_pair
                         *reinterpret_cast<uint4 *>(tile + BOX * blk + 128 * valid + 16 * r) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 } else {
-                    for (int e = lane - 1; e < 4 * PAGE * 8; e += 31)
-                        if (!((seen >> (e / 8 % PAGE)) & 1ull))
-                            *reinterpret_cast<uint4 *>(tile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+                    // 32 pieces of 16 bytes a row: lane l takes piece l, and lane 1 piece 0 too.
+                    for (unsigned long long m = ~seen; m; m &= m - 1) {
+                        uint8_t *row = tile + 128 * (__ffsll(m) - 1) + 16 * (lane % 8);
+                        *reinterpret_cast<uint4 *>(row + BOX * (lane / 8)) = make_uint4(0u, 0u, 0u, 0u);
+                        if (lane == 1) *reinterpret_cast<uint4 *>(row - 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp(0xfffffffeu);
@@ -558,6 +563,11 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
             float v[64];
             tc::tmem_ld64(tmem + TM_O + 128 * half + 64 * q + lane_addr, v);
             tc::tmem_wait_ld();
+            if (q == 1) {   // O is in registers: the next item's first PV may overwrite it
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(c.lead_bar(B_OFREE));
+            }
 #pragma unroll
             for (int jo = 0; jo < 8; ++jo) {
                 const int oct = 32 * half + 16 * hsel + 8 * q + jo;
@@ -569,9 +579,6 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
                     tc::st_global_v8(p.part_o + (((size_t)k * 64 + oct) * H + head) * 8, v + 8 * jo);
             }
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(c.lead_bar(B_OFREE));
         if (hsel == 0 && half == 0) {
             p.part_ml[((size_t)k * H + head) * 2] = m_run * 0.69314718055994531f;
             p.part_ml[((size_t)k * H + head) * 2 + 1] = l_tot;
@@ -767,7 +774,8 @@ int tc_token_granule() { return STEP; }
 
 cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *latent, const int *page_table,
                              const Plan &plan, int max_pages, int n_pages, int s_q, float *part_o, float *part_ml,
-                             int *err, int sms, cudaStream_t st, const View &view, const int *seq_lens, bool oct_layout) {
+                             int *err, int sms, cudaStream_t st, const View &view, const int *seq_lens,
+                             PartLayout parts) {
     if (plan.n_work == 0) return cudaSuccess;
     CUtensorMap tm_q, tm_k, tm_v;
     const uint64_t kv_rows = (uint64_t)n_pages * PAGE;
@@ -788,8 +796,8 @@ cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *laten
     p.withhold = g_test_withhold;
     p.view = view;
     p.seq_lens = seq_lens;
-    p.oct_stride = oct_layout ? 8 * H : 8;
-    p.head_stride = oct_layout ? 8 : 64;
+    p.oct_stride = parts == PART_OCTETS ? 8 * H : 8;
+    p.head_stride = parts == PART_OCTETS ? 8 : 64;
     auto k = view.kind == VIEW_CAUSAL ? tc_decode_kernel<false> : tc_decode_kernel<true>;
     cudaError_t e = raise_smem_limit((const void *)k, SMEM_ALLOC);
     if (e != cudaSuccess) return e;

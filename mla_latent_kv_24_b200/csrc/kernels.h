@@ -70,19 +70,24 @@ int simt_heads_per_block(const Dims &d, int mode);
 // Split combine (+ W_UV up-projection when W_uv != nullptr) (combine.cu).
 //   out [rows, H, d_v].  Output row r = (b, j) merges plan row r / qpi: partial results
 //   k * qpi + r % qpi for its work items k (qpi = 1 when every plan row is one query).
-// keep_empty: rows without work items keep what `out` holds (otherwise they become zero).
 cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part_ml,
                            const int *row_first, int rows, int qpi, int DV, const void *W_uv, void *out,
-                           cudaStream_t st, bool keep_empty = false);
+                           cudaStream_t st);
+// The views' combine + W_UV for general shapes; keep_empty: rows without work items keep what `out`
+// holds (otherwise they become zero).
+cudaError_t launch_combine_view(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
+                                int DV, const void *W_uv, void *out, cudaStream_t st, bool keep_empty);
 
-// Tensor-core combine + W_UV for bf16, d_c = 512, d_v = 128 (combine.cu).  oct_layout: the
-// partials are in the tcgen05 decode's column-octet layout [n_work, 64, H, 8] instead of
-// [n_work, H, 512].
+// Layouts of a decode's partial O: [n_work, H, 512], and the tcgen05 decode's column octets
+// [n_work, 64, H, 8] and (for a view's many rows) blocks of 64 columns [n_work, 8, H, 64].
+enum PartLayout { PART_ROWS, PART_OCTETS, PART_BLOCKS };
+
+// Tensor-core combine + W_UV for bf16, d_c = 512, d_v = 128 (combine.cu).
 // rows_host: the plan's row starts computed on the host from the host lengths (rows + 1 values),
 // or nullptr; batches of at most RowStarts::MAX rows pass them by value, which saves the kernel a
 // dependent load (the device plan still validates the lengths and reports a mismatch).
 // fine: the merged latent rows enter the product as two bf16 values each (16 bits of their value)
-// instead of one.  With combine_by_head(rows) such a call needs the [n_work, H, 512] layout.
+// instead of one; PART_BLOCKS needs it.  combine_by_head(rows): a view's many rows come as PART_BLOCKS.
 struct RowStarts {
     static constexpr int MAX = 64;
     int n;              // rows covered (0: read row_first from the workspace)
@@ -91,7 +96,7 @@ struct RowStarts {
 bool combine_by_head(int rows);
 bool combine_mma_ok(const Dims &d, int DV, bool project);
 cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *part_ml, const int *row_first,
-                               const int *rows_host, int rows, bool oct_layout, const void *W_uv, void *out,
+                               const int *rows_host, int rows, PartLayout layout, const void *W_uv, void *out,
                                cudaStream_t st, bool keep_empty = false, bool fine = false);
 
 // Per-group cache expansion (expand.cu).

@@ -14,7 +14,7 @@ cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *laten
                              const Plan &plan, int max_pages, int n_pages, int s_q, float *part_o,
                              float *part_ml, int *err, int sms, cudaStream_t st, const View &view = View{},
                              const int *seq_lens = nullptr,    // for the views other than causal
-                             bool oct_layout = true);          // false: partials [n_work, H, 512]
+                             PartLayout parts = PART_OCTETS);   // or, with a view, PART_BLOCKS
 
 // The per-head products around a view's decode for many rows (head_gemm.cu; bf16, d_nope = d_v = 128,
 // d_c = 512, d_rope = 64): launch_q_absorb_mma and launch_combine_mma (fine) on the 5th-generation tensor cores.
