@@ -62,9 +62,9 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
 
 // GQA path: the no-position part is used as is; only the RoPE part turns.  A warp takes RH heads of a
 // row: each lane forms one pair's angle, sine and cosine (in double) once for all of them.  (One angle
-// per head and pair, as before, kept the double-precision units busy for 7 us at 4 rows and 16 at 64.)
+// per head and pair took 16 us for 64 rows, this 11; RH = 1, 2, 4, 8 come within 1 us of a call.)
 // The last block builds the split plan instead.
-constexpr int RH = 8;
+constexpr int RH = 2;
 
 template <typename T>
 __global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, const int *__restrict__ seq_lens,
@@ -155,11 +155,10 @@ cudaError_t launch_q_rope(const Dims &d, const void *q, const int *seq_lens, int
 // has completed, and a second wave would start its loads only then.  More rows: a CTA keeps its W_UK
 // tile (128 columns) and walks 64-row tiles of the batch, the next tile's queries arriving while this
 // one is multiplied, and stores whole 256-byte row pieces through shared memory.  (With 64 x 64 tiles
-// of their own and 4-byte stores: 82 us for 512 rows, 29 for 128; this form PLACEHOLDER.)
+// of their own, 4-byte stores and an angle per head: 82 us for 512 rows, 29 for 128; now 48 and 19.)
 //
-// The extra columns of blocks build the split plan (their first block) and turn the queries' RoPE part:
-// a warp takes 16 heads of a row, so that each pair's double-precision angle is formed once for them
-// (forming it for every head took a third of the 512-row time).
+// The extra columns of blocks build the split plan (their first block) and turn the queries' RoPE part
+// (rope_rows.cuh), so that each pair's double-precision angle is formed once for 16 heads and more.
 // ---------------------------------------------------------------------------------------
 #include "warp_mma.cuh"
 

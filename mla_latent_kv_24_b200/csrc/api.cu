@@ -208,7 +208,10 @@ mla_status make_layout(const Dims &d, Path path, bool tc, int sms, int batch, in
             return view_row_len(hv.v.kind, hv.v.sinks, hv.v.window, lens[b], hv.n_nodes ? hv.n_nodes[b] : 0, psq, s_q,
                                 r % psq, page, INT_MAX);
         };
-        L->chunk = plan_chunk_rows(batch * psq, len, units, granule);
+        const auto rows = [=](int b) { return hv.n_nodes ? hv.n_nodes[b] : psq; };
+        const auto last_len = [=](int b) { return len(b * psq + std::max(rows(b), 1) - 1); };
+        L->chunk = tc ? plan_chunk_balanced(batch, rows, last_len, units, granule)
+                      : plan_chunk_rows(batch * psq, len, units, granule);
         const long long n = plan_count_rows(batch * psq, len, L->chunk);
         if (n > (1 << 24)) return fail(MLA_ERR_UNSUPPORTED, "too many work items (%lld)", n);
         L->n_work = (int)n;

@@ -49,6 +49,74 @@ inline int plan_chunk_rows(int rows, const Len &len, int units, int granule) {
     return (int)std::min<long long>(lo, 1 << 30);
 }
 
+// Chunk length for a view's rows on the persistent tcgen05 decode: of several candidates the one whose
+// snake-dealt items (plan_block.cuh: full chunks, then the rows' last chunks by length, longest first) give
+// the shortest longest worker.  A request has `rows(b)` rows of about `len(b)` tokens.  In steps of
+// `granule` tokens (1.9 us): an item costs its steps and ITEM_STEPS more (its queries' load, the drain of O,
+// the pipeline's refill), and the merge of its partial MERGE_STEPS over all workers (512 KiB written and
+// read).  Rows that the three-quarter rule above leaves unequal gain most: 64 ragged windows, two queries
+// each, 71 -> 57 steps; 24 trees of up to 13 nodes on 1,024 to 32,768 tokens, 265 -> 242.
+template <typename Rows, typename Len>
+inline int plan_chunk_balanced(int batch, const Rows &rows, const Len &len_of, int units, int granule) {
+    constexpr float ITEM_STEPS = 3.7f, MERGE_STEPS = 0.055f;
+    constexpr int BUCKETS = 64, MAX_UNITS = 256, KEPT = 512;
+    int kept[KEPT];   // the first requests' lengths: every candidate asks for them
+    for (int b = 0; b < std::min(batch, KEPT); ++b) kept[b] = rows(b) > 0 ? len_of(b) : 0;
+    auto len = [&](int b) { return b < KEPT ? kept[b] : len_of(b); };
+    units = std::max(1, std::min(units, MAX_UNITS));
+    auto round_up = [&](long long c) {
+        return (int)std::min<long long>(std::max<long long>(granule, (c + granule - 1) / granule * granule), 1 << 30);
+    };
+    int longest = 1;
+    long long total = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (rows(b) <= 0) continue;
+        longest = std::max(longest, len(b));
+        total += (long long)rows(b) * len(b);
+    }
+    int best = round_up(longest), tried[16], n_tried = 0;
+    float best_cost = -1.f;
+    auto consider = [&](long long candidate) {
+        const int chunk = round_up(candidate);
+        for (int i = 0; i < n_tried; ++i)
+            if (tried[i] == chunk) return;
+        tried[n_tried++] = chunk;
+        long long full = 0, items = 0;
+        int hist[BUCKETS] = {};   // the rows' last chunks by length
+        const float per_token = (float)BUCKETS / (float)chunk;
+        for (int b = 0; b < batch; ++b) {
+            const int n = rows(b), l = n > 0 ? len(b) : 0, whole = l / chunk, tail = l - whole * chunk;
+            if (l <= 0) continue;
+            full += (long long)n * whole;
+            items += (long long)n * (whole + (tail > 0));
+            if (tail) hist[std::min(BUCKETS - 1, (int)((float)tail * per_token))] += n;
+        }
+        // Equal items in whole rounds load every worker alike; the rest go on in snake order.
+        float load[MAX_UNITS] = {}, all = 0.f;
+        int at = 0, turn = 0;
+        auto deal = [&](long long n, float cost) {
+            all += cost * (float)(n / units);
+            for (int i = (int)(n % units); i > 0; --i) {
+                load[turn ? units - 1 - at : at] += cost;
+                if (++at == units) at = 0, turn ^= 1;
+            }
+        };
+        deal(full, (float)(chunk / granule) + ITEM_STEPS);
+        for (int k = BUCKETS - 1; k >= 0; --k)
+            if (hist[k]) {
+                const float steps = ((float)k + 0.5f) * (float)chunk / (float)(BUCKETS * granule);
+                deal(hist[k], std::max(1.f, (float)(int)(steps + 0.999f)) + ITEM_STEPS);
+            }
+        float worst = 0.f;
+        for (int u = 0; u < units; ++u) worst = std::max(worst, load[u]);
+        const float cost = all + worst + MERGE_STEPS * (float)items;
+        if (best_cost < 0.f || cost < best_cost) best_cost = cost, best = chunk;
+    };
+    for (int k = 1; k <= 6; ++k) consider((longest + k - 1) / k);
+    for (int k = 1; k <= 8; k *= 2) consider((total + (long long)units * k - 1) / ((long long)units * k));
+    return best;
+}
+
 // Causal rows: r = (b, j).
 inline int plan_chunk(const int32_t *lens, int batch, int s_q, int units, int granule) {
     return plan_chunk_rows(batch * s_q, [=](int r) { return lens[r / s_q] - s_q + r % s_q + 1; }, units, granule);
