@@ -248,3 +248,25 @@ def test_out_of_range_page_is_reported():
         assert e.value.status == 5
     c.table_host = keep
     check(c.upload(), "after a bad page")
+
+
+@pytest.mark.parametrize("T,ctx,nodes", [(64, (9000, 100), (64, 64)), (40, (700, 6000, 65, 64), (40, 17, 40, 33)),
+                                         (32, (130, 9000), (31, 32))])
+def test_many_rows_with_several_chunks(T, ctx, nodes):
+    # more than 96 rows merge by tiles of 128 on tcgen05, and the long request's rows have several chunks; one
+    # weight group's heads are held against the oracle, over every row
+    c = TreeCase(base_workload("dsv2", hpw=8), T, ctx, nodes, seed=360 + T).upload()
+    out = c.call(c.out(7.0))
+    mla.mla_get_device_status()
+    got = wl.from_torch_f64(out)
+    from oracle import mla as om
+    for b in range(c.B):
+        n, L = int(c.nodes[b]), int(c.lens[b])
+        rows = om.request_rows(c.inp.cache.f64(), c.inp.page_table, b, L)
+        for g in (0, 9):
+            hs = slice(8 * g, 8 * g + 8)
+            ref = om.decode_request_masked(c.inp.q.f64()[b, :n, hs], rows, c.inp.W_uk.f64()[g:g + 1],
+                                           c.inp.W_uv.f64()[g:g + 1], 8, c.w.softmax_scale, c.w.rope_base, c.positions(b),
+                                           c.visible(b))
+            assert_close(got[b, :n, hs], ref, "bf16", f"many rows T={T} request {b} group {g}")
+        assert (got[b, n:] == 7.0).all()
