@@ -416,6 +416,20 @@ __device__ void run_pv_issuer(const Ctx &c, const TcParams &p, uint32_t tmem, in
 // and, at the end, their sums through shared memory behind a named barrier.  Control flow does
 // not depend on data or on a wait's outcome: a wait that runs out only records the error, so
 // every thread always reaches every named barrier.
+__device__ __noinline__ void rescale_o(uint32_t addr, float alpha) {
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        float v[32];
+        tc::tmem_ld32(addr + 32 * q, v);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= alpha;
+        tc::tmem_st16(addr + 32 * q, reinterpret_cast<const uint32_t *>(v));
+        tc::tmem_st16(addr + 32 * q + 16, reinterpret_cast<const uint32_t *>(v) + 16);
+    }
+    tc::tmem_wait_st();
+}
+
 template <bool VIEW>
 __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int pair, int n_pairs) {
     const int t = threadIdx.x;                     // 0..255
@@ -492,17 +506,7 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
                 const float m_new = fmaxf(m_run, m_tile);
                 // With a view a row may not have seen anything yet (O and l are zero then).
                 const float alpha = VIEW && m_run == -INFINITY ? (m_new == -INFINITY ? 1.f : 0.f) : tc::ex2(m_run - m_new);
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    float v[64];
-                    const uint32_t a = tmem + TM_O + 128 * half + 64 * q + lane_addr;
-                    tc::tmem_ld64(a, v);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] *= alpha;
-                    tc::tmem_st64(a, v);
-                }
-                tc::tmem_wait_st();
+                rescale_o(tmem + TM_O + 128 * half + lane_addr, alpha);
                 l_run *= alpha;
                 m_run = m_new;
             }
