@@ -410,13 +410,11 @@ __device__ void run_pv_issuer(const Ctx &c, const TcParams &p, uint32_t tmem, in
 }
 
 // --------------------------------------------------------------------------- softmax + epilogue
-// Eight warps, two per TMEM lane quadrant: warp w reads lanes [32 (w % 4), +32) and column half
-// w / 4 of each S buffer, so thread t owns lane L = 32 (w % 4) + lane, i.e. head L % 64, tokens
-// 64 (L / 64) + 32 (w / 4) + [0, 32) of the step.  The four threads of a head swap their maxima
-// and, at the end, their sums through shared memory behind a named barrier.  Control flow does
-// not depend on data or on a wait's outcome: a wait that runs out only records the error, so
-// every thread always reaches every named barrier.
+// O x alpha for a lane's 128 columns.  Out of line: the lazy rule calls for it in few steps, and the roles share one
+// instruction cache (512 tree rows of 8256 tokens in the loop 935 us, out of it 905; short causal rows alike).  The tensor
+// memory instructions want the whole warp, which arrives together: the decision is one for the CTA.
 __device__ __noinline__ void rescale_o(uint32_t addr, float alpha) {
+    __syncwarp();
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
         float v[32];
@@ -430,6 +428,12 @@ __device__ __noinline__ void rescale_o(uint32_t addr, float alpha) {
     tc::tmem_wait_st();
 }
 
+// Eight warps, two per TMEM lane quadrant: warp w reads lanes [32 (w % 4), +32) and column half
+// w / 4 of each S buffer, so thread t owns lane L = 32 (w % 4) + lane, i.e. head L % 64, tokens
+// 64 (L / 64) + 32 (w / 4) + [0, 32) of the step.  The four threads of a head swap their maxima
+// and, at the end, their sums through shared memory behind a named barrier.  Control flow does
+// not depend on data or on a wait's outcome: a wait that runs out only records the error, so
+// every thread always reaches every named barrier.
 template <bool VIEW>
 __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int pair, int n_pairs) {
     const int t = threadIdx.x;                     // 0..255

@@ -10,7 +10,7 @@ import torch
 import mla_latent_kv_24_b200 as mla
 import workloads as wl
 from _gpu import assert_close
-from _views import TreeCase, base_workload, tree_visible
+from _views import TreeCase, WindowCase, base_workload, tree_visible
 
 pytestmark = pytest.mark.gpu
 
@@ -270,3 +270,46 @@ def test_many_rows_with_several_chunks(T, ctx, nodes):
                                            c.visible(b))
             assert_close(got[b, :n, hs], ref, "bf16", f"many rows T={T} request {b} group {g}")
         assert (got[b, n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("windowed", [False, True])
+def test_large_scores_in_causal_rows(windowed):
+    # the same for rows that see all before them, with and without a window: O is rescaled out of line in every step
+    # whose maximum rises, and columns left out of it would keep the earlier tokens' sum
+    w = base_workload("dsv2")
+    c = WindowCase(w, 4, (1400, 700), 3, 900, seed=349)
+    c.q.mul_(40.0)
+    c.inp.q.data = wl.f32_to_bf16_bits(wl.bf16_bits_to_f32(c.inp.q.data) * np.float32(40))
+    if not windowed:
+        c.sinks, c.window = 0, 1 << 20
+    c.upload()
+    out = c.out()
+    if windowed:
+        c.call(out)
+    else:
+        ws = torch.full((mla.mla_decode_workspace_size(c.dims, 2, 4, c.lens),), 255, dtype=torch.uint8, device="cuda")
+        mla.mla_decode_absorbed(c.dims, c.q, c.W_uk, c.W_uv, c.cache, c.d["page_table"], c.d["seq_lens"], c.lens, 2, 4,
+                                c.max_pages, c.n_pages, out, ws)
+    mla.mla_get_device_status()
+    got, ref = wl.from_torch_f64(out), c.reference()
+    assert np.isfinite(got).all()
+    from oracle import mla as om
+    rows_checked = rising = 0
+    for b in range(2):
+        rows = om.request_rows(c.inp.cache.f64(), c.inp.page_table, b, int(c.lens[b]))
+        for j in range(4):
+            seen = np.flatnonzero(c.visible(b)[j])
+            for h in range(0, w.H, 16):
+                q = om._q_tilde(c.inp.q.f64()[b, j, h], 128, int(c.lens[b]) - 4 + j, w.rope_base)
+                K = np.concatenate([rows[:, :512] @ c.inp.W_uk.f64()[h].T, rows[:, 512:]], 1)[seen]
+                s = K @ q * w.softmax_scale
+                rising += s[128:].max() > s[:128].max() + 20
+                top = np.sort(s)
+                q_lat = c.inp.W_uk.f64()[h].T @ q[:128]
+                off = 2 ** -8 * w.softmax_scale * (np.abs(rows[seen][:, :512]) @ np.abs(q_lat) +
+                                                   np.abs(rows[seen][:, 512:]) @ np.abs(q[128:])).max()
+                if top[-1] - top[-2] > 2 * off + 12:      # as above: the winner's weight is 1 in any rounding
+                    rows_checked += 1
+                    tol = 3 * 2 ** -8 * np.abs(c.inp.W_uv.f64()[h]) @ np.abs(rows[seen][np.argmax(s)][:512]) + 0.05
+                    assert (np.abs(got[b, j, h] - ref[b, j, h]) <= tol).all()
+    assert rows_checked > 0 and rising > 0
