@@ -326,29 +326,8 @@ __global__ void __launch_bounds__(PJ_THREADS, 2) project_tc_kernel(const __grid_
 
 // --------------------------------------------------------------------------- tensor maps
 // Boxes of 64 columns x 128 rows, 128-byte swizzle: of a row-major matrix [rows, cols], or with heads > 0 of
-// one head of [rows, heads, cols].  They depend only on the address and the sizes, and a decode loop passes
-// the same buffers every step, so recent encodings are kept.
+// one head of [rows, heads, cols].
 bool encode_box(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t heads) {
-    struct Entry {
-        const void *ptr;
-        uint64_t cols, rows, heads;
-        int device;
-        CUtensorMap map;
-    };
-    static std::mutex mu;
-    static Entry cache[32];
-    static int used = 0, next = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        for (int i = 0; i < used; ++i)
-            if (cache[i].ptr == ptr && cache[i].cols == cols && cache[i].rows == rows && cache[i].heads == heads &&
-                cache[i].device == dev) {
-                *m = cache[i].map;
-                return true;
-            }
-    }
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *f = nullptr;
         cudaDriverEntryPointQueryResult qr;
@@ -362,15 +341,9 @@ bool encode_box(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, u
     const cuuint64_t d2[2] = {cols, rows}, s2[1] = {cols * 2};
     const cuuint64_t d3[3] = {cols, heads, rows}, s3[2] = {cols * 2, cols * heads * 2};
     const cuuint32_t b2[2] = {64, TM}, b3[3] = {64, 1, TM};
-    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads ? 3 : 2, const_cast<void *>(ptr), heads ? d3 : d2, heads ? s3 : s2,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads ? 3 : 2, const_cast<void *>(ptr), heads ? d3 : d2, heads ? s3 : s2,
            heads ? b3 : b2, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    std::lock_guard<std::mutex> lock(mu);
-    cache[next] = Entry{ptr, cols, rows, heads, dev, *m};
-    next = (next + 1) % 32;
-    used = used < 32 ? used + 1 : 32;
-    return true;
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
