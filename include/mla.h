@@ -275,7 +275,8 @@ MLA_API mla_status mla_cache_reserve(const mla_dims *dims, const int32_t *new_le
  * mla_cache_fork — requests dst_req[i] become copies of what requests src_req[i] were before the call
  * (device [n_fork] each): full pages are shared (page_refs counts the new holder, dropped entries stay
  * dropped), the rows of a partly filled last page are copied into a new page, so that source and copy
- * can both grow.  The destinations must be empty (seq_lens 0), each named once; a source may be named
+ * can both grow.  A source's full pages are shared with the drafted nodes in them: fork while a source
+ * has none (before they are reserved, or after mla_cache_accept).  The destinations must be empty (seq_lens 0), each named once; a source may be named
  * many times.  A bad index or length or a destination in use (MLA_ERR_DEVICE_BOUNDS) or too few free
  * pages (MLA_ERR_NO_PAGES) leaves everything as it was.  A page id outside the pool is reported
  * (MLA_ERR_DEVICE_BOUNDS), and its rows are not copied.
@@ -300,13 +301,15 @@ MLA_API mla_status mla_cache_release(const mla_dims *dims, const int32_t *req_id
 
 /*
  * mla_cache_accept — keeps an accepted path of a tree of drafted tokens.  Request b's nodes are the
- * rows [ctx, ctx + n) with ctx = ctx_lens[b], n = n_nodes[b] <= max_nodes <= 64; its path is the
+ * rows [ctx, ctx + n) with ctx = ctx_lens[b], n = n_nodes[b] <= max_nodes <= 64, ctx + n <= seq_lens[b]
+ * (a request with n = 0 and no path takes no part, whatever ctx_lens[b] holds); its path is the
  * nodes accepted[b][0..n_accepted[b]), whose indices must rise (device [batch], [batch, max_nodes]).
  * Their rows move to ctx, ctx + 1, ... in every layer of the caches given, seq_lens[b] becomes
- * ctx + n_accepted[b], and the pages of the nodes behind it are dropped as by mla_cache_release
+ * ctx + n_accepted[b], and the pages behind that are dropped as by mla_cache_release
  * (page_refs NULL: they stay).  A request whose counts or indices are not so, or whose rows' pages
  * are out of range, is left as it was and reported (MLA_ERR_DEVICE_BOUNDS).  The rows written lie
- * behind the context, in pages that belong to the request alone (mla_cache_fork sees to that).
+ * behind the context, in pages that belong to the request alone (a fork before the nodes were reserved
+ * sees to that).
  */
 MLA_API mla_status mla_cache_accept(const mla_dims *dims, const int32_t *ctx_lens, const int32_t *n_nodes,
                                     const int32_t *accepted, const int32_t *n_accepted, int32_t max_nodes,

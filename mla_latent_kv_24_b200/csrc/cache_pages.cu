@@ -7,6 +7,10 @@
 // it takes (4 bytes a page: 40,000 pages are 160 KB); one block does it, 16,384 pages at a time.
 //
 // Rows of the caches are copied with 16-byte accesses (2 or 4 bytes where a row's size asks for it).
+// These kernels write lengths and page-table entries, which the kernels of the next call may read as
+// inputs before they wait for their predecessor.  So none but the fork's first lets its successor
+// launch before all its blocks have ended, and each makes its writes visible to the device first.
+//
 // All of it is bound by launches and latency, except forks over many layers, which are bound by the
 // copied bytes.
 #include <cooperative_groups.h>
@@ -121,7 +125,7 @@ __device__ __forceinline__ uint32_t first_bits(const Pool &p) {
 
 // ------------------------------------------------------------------------------------- reserve
 __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restrict__ new_lens) {
-    step_begin();
+    step_wait_prev();
     __shared__ int off[CAP + 1];
     const uint32_t tile = first_bits(p);
     const int per = ceil_div(p.batch, PT), b0 = min(p.batch, (int)threadIdx.x * per), b1 = min(p.batch, b0 + per);
@@ -165,6 +169,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restri
     }
     __syncthreads();   // the lengths are read above
     for (int b = b0; b < b1; ++b) p.seq_lens[b] = new_lens[b];
+    __threadfence();
 }
 
 // ------------------------------------------------------------------------------------- fork
@@ -249,11 +254,14 @@ __device__ __forceinline__ void copy_span(char *dst, const char *src, size_t byt
 // fewer pieces than blocks.
 __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
                                                         RowSets sets) {
-    step_begin();
+    step_wait_prev();
     const int rank = blockIdx.x, blocks = gridDim.x;              // the cluster spans the grid's x
     const int s = src[blockIdx.y], d = dst[blockIdx.y];
-    int L = 0;
-    if (s >= 0 && s < p.batch && d >= 0 && d < p.batch) L = -1 - p.seq_lens[d];   // <= 0: refused as a whole, or empty
+    int L = -1;   // < 0: refused as a whole
+    if (s >= 0 && s < p.batch && d >= 0 && d < p.batch) {
+        L = -1 - p.seq_lens[d];
+        if (L > 0 && L != p.seq_lens[s]) L = -1;   // no marker: a length that cannot be, which refused the call
+    }
     if (L > 0) {
         const int full = L / p.page, rem = L % p.page;
         for (int k = rank * (int)blockDim.x + (int)threadIdx.x; k < full; k += blocks * (int)blockDim.x) {
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__res
         }
         if (rem && sets.n) {
             const int from = *p.entry(s, full), to = *p.entry(d, full);
-            if (from < 0 || from >= p.n_pages) {
+            if (from < 0 || from >= p.n_pages || to < 0 || to >= p.n_pages) {
                 if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
             } else {
 #pragma unroll
@@ -289,7 +297,8 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__res
         }
     }
     cooperative_groups::this_cluster().sync();   // every block has read the length's marker
-    if (rank == 0 && threadIdx.x == 0 && d >= 0 && d < p.batch && s >= 0 && s < p.batch && L >= 0) p.seq_lens[d] = L;
+    if (rank == 0 && threadIdx.x == 0 && L >= 0) p.seq_lens[d] = L;
+    __threadfence();
 }
 
 // ------------------------------------------------------------------------------------- release
@@ -309,7 +318,7 @@ __device__ __forceinline__ void drop_entry(const Pool &p, int *entry) {
 
 __global__ void __launch_bounds__(256) release_kernel(Pool p, const int *__restrict__ req, const int *__restrict__ first,
                                                       const int *__restrict__ last) {
-    step_begin();
+    step_wait_prev();
     const int b = req[blockIdx.x];
     if (b < 0 || b >= p.batch) {
         if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
@@ -330,14 +339,16 @@ __global__ void __launch_bounds__(256) release_kernel(Pool p, const int *__restr
         __syncthreads();
         if (threadIdx.x == 0) p.seq_lens[b] = 0;
     }
+    __threadfence();
 }
 
 // ------------------------------------------------------------------------------------- accept
-// Whether request b's accepted path is one: node indices that rise and exist, in pages that it has.
-// The same answer in every block of a call.  All threads of the block call it.
-__device__ __forceinline__ bool path_ok(const Pool &p, int b, int ctx, int n, const int *acc, int n_acc, int max_nodes) {
+// Whether the accepted path of a request of length L is one: rows it has, node indices that rise and exist, in
+// pages of the pool.  The same answer in every block of a call.  All threads of the block call it.
+__device__ __forceinline__ bool path_ok(const Pool &p, int b, int L, int ctx, int n, const int *acc, int n_acc,
+                                        int max_nodes) {
     int bad = 0;
-    if (n < 0 || n > max_nodes || n_acc < 0 || n_acc > n || ctx < 0 || (long long)ctx + n > (long long)p.max_pages * p.page)
+    if (n < 0 || n > max_nodes || n_acc < 0 || n_acc > n || !p.fits(L) || ctx < 0 || (long long)ctx + n > L)
         bad = 1;
     else
         for (int k = threadIdx.x; k < n_acc; k += blockDim.x) {
@@ -384,11 +395,13 @@ constexpr int ACCEPT_THREADS = 288;   // 8 x 288 columns: the latent rows of 32 
 __global__ void __launch_bounds__(ACCEPT_THREADS, 4) accept_kernel(Pool p, const int *__restrict__ ctx_lens,
                                                      const int *__restrict__ n_nodes, const int *__restrict__ accepted,
                                                      const int *__restrict__ n_accepted, int max_nodes, RowSets sets) {
-    step_begin();
+    step_wait_prev();
     const int rank = blockIdx.x, blocks = gridDim.x, b = blockIdx.y;
     const int ctx = ctx_lens[b], n = n_nodes[b], n_acc = n_accepted[b];
     const int *acc = accepted + (size_t)b * max_nodes;
-    const bool ok = path_ok(p, b, ctx, n, acc, n_acc, max_nodes);
+    if (n == 0 && n_acc == 0) return;   // takes no part (the whole cluster)
+    const int L = p.seq_lens[b];
+    const bool ok = path_ok(p, b, L, ctx, n, acc, n_acc, max_nodes);
     __shared__ Moves m;
     __shared__ int n_move;
     if (threadIdx.x == 0) n_move = 0;
@@ -419,9 +432,10 @@ __global__ void __launch_bounds__(ACCEPT_THREADS, 4) accept_kernel(Pool p, const
         return;
     }
     if (p.refs)
-        for (int k = p.pages_of(ctx + n_acc) + (int)threadIdx.x; k < p.pages_of(ctx + n); k += blockDim.x)
+        for (int k = p.pages_of(ctx + n_acc) + (int)threadIdx.x; k < p.pages_of(L); k += blockDim.x)
             drop_entry(p, p.entry(b, k));
     if (threadIdx.x == 0) p.seq_lens[b] = ctx + n_acc;
+    __threadfence();
 }
 
 Pool pool_of(const PagePool &a) {

@@ -62,12 +62,18 @@ __device__ __forceinline__ void step_begin() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 // The split form, for kernels whose loads touch only the caller's inputs (weights, queries, hidden
-// states, lengths, page tables), which no kernel of this library writes: they let the next kernel
-// launch at once, load and compute while the previous kernel finishes, and call step_wait_prev()
-// before their first store.  Every thread that stores calls it, so the kernel completes only after
+// states, lengths): they let the next kernel launch at once, load and compute while the previous
+// kernel finishes, and call step_wait_prev() before their first store.  The kernels of this library
+// that write lengths never launch their successor early (cache_pages.cu), and lengths that are read
+// before the wait are read past the SM's own cache (load_len).  Every thread that stores calls it, so the kernel completes only after
 // its predecessor has, and ordering down the stream stays that of a plain stream.
 __device__ __forceinline__ void step_allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void step_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ int load_len(const int *p) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 
 // ---------------------------------------------------------------------------------------
 // Split-KV plan.  Row r = (b, j) has len_r = seq_lens[b] - s_q + j + 1 visible tokens and
@@ -106,7 +112,7 @@ struct Plan {
 
 namespace mla {
 // Launches `kernel` on `st` with programmatic stream serialisation (the kernel must call
-// step_begin() first).  Host only.
+// step_begin() or step_wait_prev(), as above).  Host only.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_step(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                                Args &&...args) {

@@ -10,8 +10,8 @@ namespace mla {
 // Position of query j of request b: the s_q queries are the request's last tokens, and a tree's
 // node sits at its depth behind the context.
 __device__ __forceinline__ int query_pos(const View &v, const int *seq_lens, int b, int j, int s_q) {
-    if (v.kind == VIEW_TREE) return seq_lens[b] - v.n_nodes[b] + v.depths[(size_t)b * s_q + j];
-    return seq_lens[b] - s_q + j;
+    if (v.kind == VIEW_TREE) return load_len(seq_lens + b) - v.n_nodes[b] + v.depths[(size_t)b * s_q + j];
+    return load_len(seq_lens + b) - s_q + j;
 }
 
 constexpr int ROPE_D_QK = 192, ROPE_D_OUT = 576;

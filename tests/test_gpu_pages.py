@@ -377,3 +377,100 @@ def test_a_captured_round_replays():
     mla.mla_get_device_status()
     p.check()
     del g
+
+
+def test_accept_takes_no_nodes_that_a_request_does_not_have():
+    # a context too long would drop pages that the request never had; what lies behind the nodes goes with its pages
+    for ctx in ((60, 101, 10), (60, 300, 10), (60, 2 ** 31 - 1, 10)):
+        p = Pool("dsv2", (60, 100, 10), 30, slack=3, seed=9)
+        p.both("reserve", (68, 108, 18))
+        p.accept(ctx, (8, 8, 8), ([0, 2, 5],) * 3, 8)
+        refused(5)
+        p.m_accept((60, 0, 10), (8, 0, 8), ([0, 2, 5], [], [0, 2, 5]))
+        p.lens[1] = 108
+        p.check()
+    p = Pool("dsv2", (60, 100, 10), 30, slack=3, seed=9)
+    p.both("reserve", (68, 260, 18))
+    p.accept((60, 20, 10), (8, 8, 8), ([0, 2, 5],) * 3, 8)
+    mla.mla_get_device_status()
+    p.m_accept((60, 20, 10), (8, 8, 8), ([0, 2, 5],) * 3)
+    p.m_drop(1, 1, 5)
+    p.check()
+    p = Pool("dsv2", (60, 100, 10), 30, slack=3, seed=9)
+    p.both("reserve", (68, 100, 18))
+    p.accept((60, 0, 10), (8, 0, 8), ([0, 2, 5], [], [0, 2, 5]), 8)    # without nodes: takes no part, whatever ctx is
+    mla.mla_get_device_status()
+    p.m_accept((60, 100, 10), (8, 0, 8), ([0, 2, 5], [], [0, 2, 5]))
+    p.check()
+
+
+def test_a_fork_refused_for_a_length_that_cannot_be_leaves_it():
+    p = Pool("dsv2", (100, 64, 0, 0), 8)
+    p.lens[2] = -101                                                    # what a carried-out fork of request 0 notes
+    p.upload()
+    p.fork((1, 1), (2, 3))
+    refused(5)
+    p.check()
+
+
+@pytest.mark.parametrize("B", [2, 40])
+@pytest.mark.parametrize("op", ["causal", "window", "tree", "grouped", "append"])
+def test_a_call_right_behind_one_that_changes_lengths(op, B):
+    # reserve -> accept (trims) -> the call, with no host or other kernel between; held against the same calls with
+    # the host waiting after each.  The calls' first kernels read lengths before their predecessor has ended.
+    ctx, n = 130 + 5 * np.arange(B), 8
+    p = Pool("dsv2", (0,) * B, 6 * B + 3, slack=6 + 5 * B // 64, seed=11, expanded=op == "grouped")
+    d, T = p.dims, 2
+    g = torch.Generator().manual_seed(4)
+    rnd = lambda *s: torch.randn(s, generator=g).mul_(0.2).to(torch.bfloat16).cuda()  # noqa: E731
+    q, W_uk, W_uv = rnd(B, T, 128, 192), rnd(16, 128, 512), rnd(16, 128, 512)
+    lens = (ctx + T).astype(np.int32)
+    full, d_ctx, nodes, n_acc = p.i32(ctx + n), p.i32(ctx), p.i32([n] * B), p.i32([T] * B)
+    acc = torch.arange(n, dtype=torch.int32, device="cuda").repeat(B, 1)
+    every, t_nodes, depths = p.i32(range(B)), p.i32([T] * B), p.i32([0, 1] * B)
+    mask = torch.tensor([1, 3] * B, dtype=torch.int64, device="cuda")
+    out = torch.empty(B, T, 128, 128, dtype=torch.bfloat16, device="cuda")
+    size = {"causal": lambda: mla.mla_decode_workspace_size(d, B, T, lens),
+            "window": lambda: mla.mla_decode_window_workspace_size(d, B, T, 4, 100, lens),
+            "tree": lambda: mla.mla_decode_tree_workspace_size(d, B, T, lens, [T] * B),
+            "grouped": lambda: mla.gqla_decode_window_workspace_size(d, B, T, 4, 100, lens),
+            "append": lambda: 256}[op]()
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    h, W = rnd(B, 512), rnd(576, 512)
+    where = (p.d_table, p.d_lens, lens, B, T)
+    cache = p.d_lat[0]
+
+    def step(wait):
+        mla.mla_cache_reserve(d, full, *p.tail())
+        wait()
+        if op != "append":
+            mla.mla_cache_accept(d, d_ctx, nodes, acc, n_acc, n, *p.tail(), p.d_lat, None, 1)
+            wait()
+        if op == "causal":
+            mla.mla_decode_absorbed(d, q, W_uk, W_uv, cache, *where, p.max_pages, p.n_pages, out, ws)
+        elif op == "window":
+            mla.mla_decode_window(d, q, W_uk, W_uv, cache, *where, 4, 100, p.max_pages, p.n_pages, out, ws)
+        elif op == "tree":
+            mla.mla_decode_tree(d, q, W_uk, W_uv, cache, p.d_table, p.d_lens, t_nodes, lens, [T] * B, depths, mask, B, T,
+                                p.max_pages, p.n_pages, out, ws)
+        elif op == "grouped":
+            mla.gqla_decode_window(d, q, p.d_exp[0], cache, *where, 4, 100, p.max_pages, p.n_pages, out, ws)
+        else:
+            mla.mla_cache_append(d, h, 512, W[:512], W[512:], every, d_ctx, B, p.d_table, B, p.max_pages, p.n_pages, cache)
+        wait()
+        mla.mla_cache_release(d, every, None, None, B, *p.tail())
+        wait()
+
+    result = cache if op == "append" else out
+    step(torch.cuda.synchronize)
+    mla.mla_get_device_status()
+    want = result.clone()
+    assert op == "append" or want.float().abs().sum() > 0
+    for _ in range(20):
+        if op != "append":
+            out.zero_()
+        step(lambda: None)
+        step(lambda: None)
+        mla.mla_get_device_status()
+        assert torch.equal(result, want)
+    assert (p.d_refs == 0).all() and (p.d_lens == 0).all()
