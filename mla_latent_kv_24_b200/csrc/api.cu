@@ -421,9 +421,8 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
             MLA_CUDA(launch_q_absorb(d, q, W_uk, seq_lens, batch, s_q, qp, st, hv.v), "launch q_absorb");
         }
         // A view's rows are merged by the kernel that suits their number, each from its own layout.
-        const PartLayout parts = !tc                                                             ? PART_ROWS
-                                 : hv.v.kind != VIEW_CAUSAL && combine_by_head(L.rows) ? PART_BLOCKS
-                                                                                       : PART_OCTETS;
+        PartLayout parts = tc ? PART_OCTETS : PART_ROWS;
+        if (tc && hv.v.kind != VIEW_CAUSAL && project_tc_pays(L.rows, L.n_work)) parts = PART_BLOCKS;
         if (tc) {
             ProfileScope prof(st);
             MLA_CUDA(launch_tc_decode(d, qp, latent, page_table, plan, max_pages, n_pages, s_q, part_o, part_ml, err, sms,
@@ -435,8 +434,8 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
                              hv.v, seq_lens};
             MLA_CUDA(launch_decode_simt(d, a, st), "launch decode (CUDA cores)");
         }
-        if (parts == PART_BLOCKS && project_tc_pays(L.rows)) {
-            MLA_CUDA(launch_project_tc(d, part_o, part_ml, row_first, L.rows, W_uv, out, err, st, keep_empty),
+        if (parts == PART_BLOCKS) {
+            MLA_CUDA(launch_project_tc(d, part_o, part_ml, row_first, L.rows, W_uv, out, err, sms, st, keep_empty),
                      "launch merge + W_UV (tcgen05)");
         } else if (combine_mma_ok(d, L.DV, true)) {
             // The plan's row starts from the host lengths (the device plan is built from the same rule).

@@ -273,7 +273,9 @@ constexpr int CM_ROWS = 32, CM_FINE = 16;                 // rows per tile
 constexpr int XS = 4, XC = CK / XS, X_LD = XC + 8;        // cluster size, columns per CTA, smem row
 
 // OCT: partials in the column-octet layout [k][64][H][8] of the tcgen05 decode (else [k][H][512]).
-// FINE: the merged rows enter the product as hi + lo (see project_rows_kernel below).
+// FINE: a merged value x enters the product as two bf16 values hi = bf16(x), lo = bf16(x - hi), so that the product
+// adds no rounding of its own to the output's (with hi alone the outputs of trees and windows were 0.0030 off in
+// relative norm instead of 0.0025).
 template <bool OCT, bool FINE, int CM>
 __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
     combine_split_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ml,
@@ -409,168 +411,7 @@ __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
     cluster.sync();   // the other CTAs' products stay alive until every CTA has read them
 }
 
-// ---------------------------------------------------------------------------------------
-// Merge + W_UV for the trees' and windows' decodes, whose batches have up to thousands of rows.
-//
-// One CTA takes a head and PM rows and walks the latent in four slices of 128 columns.  Per slice it
-// merges the rows' chunk partials ([item][8][H][64] fp32; a row with one chunk, the usual case, is only
-// scaled by 1 / l), splits each merged value x into two bf16 values hi = bf16(x), lo = bf16(x - hi), and adds (hi + lo) W_UV[w][:, slice]^T with
-// mma.sync m16n8k16: the merged latent keeps 16 bits of its value, so that the product adds no
-// rounding of its own to the output's (with hi alone the outputs were 0.0030 off in relative norm
-// instead of 0.0025).  The next slice's partials are in flight in registers and its W_UV tile by
-// cp.async while this one is multiplied.
-//
-// Bound by reading the partials once (256 KiB a row) and W_UV once per PM rows (from L2).  The cluster
-// kernel above spends a memory round trip on every eighth row: 291 us for 512 rows of one chunk, 80 us
-// for 128; this one 81 and 26.  (Above 96 rows project_tc_kernel takes over.)
-// ---------------------------------------------------------------------------------------
-constexpr int PW_LD = XC + 8;
-
-template <int PM>
-__global__ void __launch_bounds__(256) project_rows_kernel(const float *__restrict__ part_o,
-                                                           const float *__restrict__ part_ml,
-                                                           const int *__restrict__ row_first, int rows, int H,
-                                                           const __nv_bfloat16 *__restrict__ W_uv, int hpw,
-                                                           __nv_bfloat16 *__restrict__ out, bool keep_empty) {
-    constexpr int TPR = 256 / PM;            // threads of a row
-    constexpr int F4 = XC / 4 / TPR;         // float4 a thread holds of its row's slice
-    step_allow_next();
-    extern __shared__ __align__(16) uint8_t psm[];
-    __nv_bfloat16 *Ws = reinterpret_cast<__nv_bfloat16 *>(psm);      // [2][128 v][128 c + 8]
-    __nv_bfloat16 *Hi = Ws + 2 * CN * PW_LD, *Lo = Hi + PM * PW_LD;  // [PM][128 c + 8]
-    const int h = blockIdx.x, row0 = blockIdx.y * PM;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const __nv_bfloat16 *W = W_uv + (size_t)(h / hpw) * CN * CK;
-    auto load_w = [&](int s) {
-        for (int c = tid; c < CN * XC / 8; c += 256) {
-            const int v = c / (XC / 8), k = (c % (XC / 8)) * 8;
-            cp_async16(Ws + (s & 1) * CN * PW_LD + v * PW_LD + k, W + (size_t)v * CK + s * XC + k, true);
-        }
-        cp_async_commit();
-    };
-    load_w(0);   // an input: streams in while the decode finishes
-    step_wait_prev();
-    // This thread's row: chunks [k0, k1), the merged maximum and 1 / sum.
-    const int r = tid / TPR, sub = tid % TPR, row = row0 + r;
-    int k0 = 0, k1 = 0;
-    if (row < rows) k0 = row_first[row], k1 = row_first[row + 1];
-    const float2 *ml = reinterpret_cast<const float2 *>(part_ml);
-    float2 first = make_float2(-INFINITY, 0.f);
-    if (k0 < k1) first = ml[(size_t)k0 * H + h];
-    auto at4 = [&](int k, int s, int i) {   // this thread's i-th float4 of chunk k, slice s
-        const int c = sub + i * TPR;          // 0..31: two blocks of 64 columns
-        return reinterpret_cast<const float4 *>(part_o + (((size_t)k * 8 + 2 * s + c / 16) * H + h) * 64) + c % 16;
-    };
-    float4 x[F4];
-    auto load_first = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < F4; ++i) x[i] = k0 < k1 ? __ldcs(at4(k0, s, i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    load_first(0);
-    float M = first.x, den = first.y;
-    for (int k = k0 + 1; k < k1; ++k) {
-        const float2 v = ml[(size_t)k * H + h];
-        const float Mn = fmaxf(M, v.x);
-        if (Mn == -INFINITY) continue;   // nothing seen so far
-        den = den * expf(M - Mn) + v.y * expf(v.x - Mn);
-        M = Mn;
-    }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    const float w0 = first.x == -INFINITY ? 0.f : expf(first.x - M) * inv;
-
-    const int wm = warp % (PM / 16), wn = warp / (PM / 16);   // warp tile: 16 rows x NW columns
-    constexpr int NW = CN / (8 / (PM / 16)), NT = NW / 8;
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-#pragma unroll 1
-    for (int s = 0; s < CK / XC; ++s) {
-#pragma unroll
-        for (int i = 0; i < F4; ++i) x[i].x *= w0, x[i].y *= w0, x[i].z *= w0, x[i].w *= w0;
-        for (int k = k0 + 1; k < k1; ++k) {
-            const float mk = ml[(size_t)k * H + h].x;
-            const float wk = mk == -INFINITY ? 0.f : expf(mk - M) * inv;
-#pragma unroll
-            for (int i = 0; i < F4; ++i) {
-                const float4 v = __ldcs(at4(k, s, i));
-                x[i].x += wk * v.x, x[i].y += wk * v.y, x[i].z += wk * v.z, x[i].w += wk * v.w;
-            }
-        }
-        __syncthreads();   // the previous slice's products are done with Hi, Lo and its W tile
-#pragma unroll
-        for (int i = 0; i < F4; ++i) {
-            const float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float lo[4];
-            uint32_t hp[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                hp[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                lo[2 * e] = v[2 * e] - __uint_as_float(hp[e] << 16);
-                lo[2 * e + 1] = v[2 * e + 1] - __uint_as_float(hp[e] & 0xffff0000u);
-            }
-            const int c = 4 * (sub + i * TPR);
-            *reinterpret_cast<uint2 *>(Hi + r * PW_LD + c) = make_uint2(hp[0], hp[1]);
-            *reinterpret_cast<uint2 *>(Lo + r * PW_LD + c) = make_uint2(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]));
-        }
-        if (s + 1 < CK / XC) {
-            load_w(s + 1);
-            load_first(s + 1);
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
-        }
-        __syncthreads();
-        const __nv_bfloat16 *Wt = Ws + (s & 1) * CN * PW_LD;
-#pragma unroll
-        for (int kk = 0; kk < XC; kk += 16) {
-            uint32_t ah[4], al[4];
-            const int ar = (wm * 16 + (lane % 8) + 8 * ((lane / 8) % 2)) * PW_LD + kk + 8 * (lane / 16);
-            ldmatrix_x4(ah[0], ah[1], ah[2], ah[3], Hi + ar);
-            ldmatrix_x4(al[0], al[1], al[2], al[3], Lo + ar);
-#pragma unroll
-            for (int j = 0; j < NT; j += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldmatrix_x4(b0, b1, b2, b3,
-                            Wt + (wn * NW + j * 8 + (lane % 8) + 8 * (lane / 16)) * PW_LD + kk + 8 * ((lane / 8) % 2));
-                mma_bf16(acc[j], ah, b0, b1);
-                mma_bf16(acc[j + 1], ah, b2, b3);
-                mma_bf16(acc[j], al, b0, b1);
-                mma_bf16(acc[j + 1], al, b2, b3);
-            }
-        }
-    }
-    const int gid = lane / 4, t4 = lane % 4;
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-        const int ro = row0 + wm * 16 + gid + 8 * hr;
-        if (ro >= rows || (keep_empty && row_first[ro] == row_first[ro + 1])) continue;
-        __nv_bfloat16 *dst = out + ((size_t)ro * H + h) * CN + wn * NW + 2 * t4;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<uint32_t *>(dst + 8 * j) = pack_bf16(acc[j][2 * hr], acc[j][2 * hr + 1]);
-    }
-}
-
-template <int PM>
-cudaError_t launch_project(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
-                           const void *W_uv, void *out, cudaStream_t st, bool keep_empty) {
-    const size_t smem = sizeof(__nv_bfloat16) * (size_t)(2 * CN + 2 * PM) * PW_LD;
-    auto k = project_rows_kernel<PM>;
-    cudaError_t e = raise_smem_limit((const void *)k, smem);
-    if (e != cudaSuccess) return e;
-    if (ceil_div(rows, PM) > 65535) return cudaErrorInvalidValue;
-    MLA_STEP_LAUNCH(k, dim3(d.H, ceil_div(rows, PM)), dim3(256), smem, st, part_o, part_ml, row_first, rows, d.H,
-                    (const __nv_bfloat16 *)W_uv, d.hpw, (__nv_bfloat16 *)out, keep_empty);
-    return cudaGetLastError();
-}
-
 }  // namespace
-
-// One 16-row tile in the cluster kernel, from octets; more rows by head (8 rows: 31.7 us a call in clusters,
-// 49.8 by head; 16: 36.0 and 41.6; 32: 48.9 and 44.7).
-bool combine_by_head(int rows) { return rows > CM_FINE; }
 
 bool combine_mma_ok(const Dims &d, int DV, bool project) {
     return project && d.bf16 && DV == CK && d.d_v == CN;
@@ -580,8 +421,6 @@ cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *
                                const int *rows_host, int rows, PartLayout layout, const void *W_uv, void *out,
                                cudaStream_t st, bool keep_empty, bool fine) {
     if (rows <= 0) return cudaSuccess;
-    if (layout == PART_BLOCKS)
-        return launch_project<64>(d, part_o, part_ml, row_first, rows, W_uv, out, st, keep_empty);
     RowStarts rs;
     rs.n = 0;
     if (rows_host != nullptr && rows <= RowStarts::MAX) {

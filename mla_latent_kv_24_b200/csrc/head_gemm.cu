@@ -176,7 +176,10 @@ enum { P_FULL = 0, P_EMPTY = 2, P_COUNT = 4 };
 
 constexpr int PJ_THREADS = 512;
 
-__global__ void __launch_bounds__(PJ_THREADS, 2) project_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
+// AHEAD: a row's second chunk is fetched a block ahead like its first, in registers that leave room for one CTA
+// on an SM.
+template <bool AHEAD>
+__global__ void __launch_bounds__(PJ_THREADS, AHEAD ? 1 : 2) project_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                             const float *__restrict__ part_o,
                                                             const float *__restrict__ part_ml,
                                                             const int *__restrict__ row_first, int rows, int H, int hpw,
@@ -218,8 +221,8 @@ __global__ void __launch_bounds__(PJ_THREADS, 2) project_tc_kernel(const __grid_
     constexpr int NR = TM * 16 / PJ_THREADS, RS = TM / NR;
     const int c4 = tid % 16, r0 = tid / 16;
     const float4 *src[NR];
-    float w0[NR];
-    uint32_t held = 0;   // bit i: row i has a chunk
+    float w0[NR], w1[NR];
+    uint32_t held = 0;   // bit i: row i has a chunk, bit NR + i: a second one
     int most = 0;        // chunks of this thread's row with the most
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
@@ -227,14 +230,24 @@ __global__ void __launch_bounds__(PJ_THREADS, 2) project_tc_kernel(const __grid_
         src[i] = reinterpret_cast<const float4 *>(part_o + ((size_t)k * KB * H + h) * 64) + c4;
         w0[i] = w0s[r];
         held |= (uint32_t)(k < k1s[r]) << i;
+        w1[i] = 0.f;
+        if (AHEAD && k + 1 < k1s[r]) {
+            held |= 1u << (NR + i);
+            const float m1 = ml[(size_t)(k + 1) * H + h].x;
+            w1[i] = m1 == -INFINITY ? 0.f : expf(m1 - ms[r]) * invs[r];
+        }
         most = max(most, k1s[r] - k);
     }
     const size_t step = (size_t)H * 16;   // float4s from one block of 64 columns to the next
-    float4 x[NR];
+    float4 x[NR], x1[NR];
     auto load_first = [&](int kb) {
 #pragma unroll
         for (int i = 0; i < NR; ++i)
             x[i] = (held >> i) & 1u ? __ldcs(src[i] + kb * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (AHEAD)
+                x1[i] = (held >> (NR + i)) & 1u ? __ldcs(src[i] + (KB + kb) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load_first(0);
     bool ok = true;
@@ -245,8 +258,13 @@ __global__ void __launch_bounds__(PJ_THREADS, 2) project_tc_kernel(const __grid_
         if (kb >= 2 && !tc::mbar_wait(bar(P_EMPTY + st), ((kb >> 1) - 1) & 1, WAIT_NS)) ok = false;
 #pragma unroll
         for (int i = 0; i < NR; ++i) x[i].x *= w0[i], x[i].y *= w0[i], x[i].z *= w0[i], x[i].w *= w0[i];
+        if (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+                x[i].x += w1[i] * x1[i].x, x[i].y += w1[i] * x1[i].y, x[i].z += w1[i] * x1[i].z, x[i].w += w1[i] * x1[i].w;
+        }
         // Further chunks: the e-th of every row together.
-        for (int e = 1; e < most; ++e) {
+        for (int e = AHEAD ? 2 : 1; e < most; ++e) {
             float4 y[NR];
             float wk[NR];
 #pragma unroll
@@ -351,10 +369,11 @@ bool encode_box(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, u
 // Above 16 rows, where the mma.sync form leaves its single wave (24 rows: 48.9 us a call against 50.6; 96: 80.2
 // and 84.2; the kernel alone at 512 rows: 35 and 48).
 bool absorb_tc_pays(int rows) { return rows > 16; }
-// A few rows with several chunks each merge faster in 64-row tiles whose threads have no products to issue
-// (24 rows: 41.4 us a call against 48.9; 48: 50.1 and 49.0; 96: 78.6 and 80.2; the kernels alone at 128 rows:
-// 26 and 21, at 512: 80 and 58).
-bool project_tc_pays(int rows) { return rows > 96; }
+// One 16-row tile merges faster in clusters of four CTAs a head (launch_combine_mma; a window's call of 8 rows 29 us
+// against 43, of 16 rows 34 and 37).  Above that a cluster takes its rows one pass after another, and this kernel a
+// row's chunks: rows^2 / 6 chunks in all are where the two meet (17 rows of 4.4 chunks 55 us in clusters, 65 here; 20
+// of 3.7: 57 and 62; 24 of 3.1: 65 and 64; 24 of one: 43 and 35; 32: 74 and 64; 40: 91 and 78).
+bool project_tc_pays(int rows, long long n_work) { return rows > 16 && 6 * n_work <= (long long)rows * rows; }
 
 cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch, int s_q,
                              void *q_abs, const PlanArgs &plan, cudaStream_t st) {
@@ -373,13 +392,16 @@ cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, con
 }
 
 cudaError_t launch_project_tc(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
-                              const void *W_uv, void *out, int *err, cudaStream_t st, bool keep_empty) {
+                              const void *W_uv, void *out, int *err, int sms, cudaStream_t st, bool keep_empty) {
     if (ceil_div(rows, TM) > 65535) return cudaErrorInvalidValue;
     CUtensorMap tm_w;
     if (!encode_box(&tm_w, W_uv, D_C, (uint64_t)d.n_groups() * D_V, 0)) return cudaErrorInvalidValue;
-    cudaError_t e = raise_smem_limit((const void *)project_tc_kernel, PJ_SMEM);
+    // With a CTA per SM or fewer, its registers may be twice as many: 128 rows of one chunk 129 -> 122 us a call, of two
+    // 170 -> 155.
+    const auto kernel = d.H * ceil_div(rows, TM) <= sms ? project_tc_kernel<true> : project_tc_kernel<false>;
+    cudaError_t e = raise_smem_limit((const void *)kernel, PJ_SMEM);
     if (e != cudaSuccess) return e;
-    MLA_STEP_LAUNCH(project_tc_kernel, dim3(d.H, ceil_div(rows, TM)), dim3(PJ_THREADS), PJ_SMEM, st, tm_w, part_o, part_ml,
+    MLA_STEP_LAUNCH(kernel, dim3(d.H, ceil_div(rows, TM)), dim3(PJ_THREADS), PJ_SMEM, st, tm_w, part_o, part_ml,
                     row_first, rows, d.H, d.hpw, (__nv_bfloat16 *)out, keep_empty, err);
     return cudaGetLastError();
 }

@@ -87,13 +87,12 @@ enum PartLayout { PART_ROWS, PART_OCTETS, PART_BLOCKS };
 // or nullptr; batches of at most RowStarts::MAX rows pass them by value, which saves the kernel a
 // dependent load (the device plan still validates the lengths and reports a mismatch).
 // fine: the merged latent rows enter the product as two bf16 values each (16 bits of their value)
-// instead of one; PART_BLOCKS needs it.  combine_by_head(rows): a view's many rows come as PART_BLOCKS.
+// instead of one.  (A view's many rows come as PART_BLOCKS and are merged by launch_project_tc.)
 struct RowStarts {
     static constexpr int MAX = 64;
     int n;              // rows covered (0: read row_first from the workspace)
     int v[MAX + 1];
 };
-bool combine_by_head(int rows);
 bool combine_mma_ok(const Dims &d, int DV, bool project);
 cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *part_ml, const int *row_first,
                                const int *rows_host, int rows, PartLayout layout, const void *W_uv, void *out,

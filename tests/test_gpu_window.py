@@ -159,3 +159,15 @@ def test_lengths_that_contradict_the_host_are_reported():
     with pytest.raises(mla.MlaError) as e:
         mla.mla_get_device_status()
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("B", [17, 24, 130])
+def test_rows_of_several_chunks_under_either_merge(B):
+    # a few more rows than one tile of the clusters' merge, with many chunks (17) or some (24), and more rows than one
+    # tile of the other
+    lens = [1400 - 7 * b for b in range(B - 1)] + [1] if B < 100 else [300 - b for b in range(B)]
+    c = WindowCase(base_workload("gqla"), 1, lens, 70, 1000, seed=484 + B)
+    c.free_unseen()
+    out = c.upload().call(c.out())
+    mla.mla_get_device_status()
+    assert_close(wl.from_torch_f64(out), c.reference(), "bf16", f"window, {B} rows")
