@@ -7,7 +7,9 @@
 // for each of the H heads.  A decode over a tree of 64 nodes and 8 requests has 512 rows, so that a head's
 // products are 128-row tiles of tcgen05.mma (one CTA, cta_group::1); on mma.sync they ran at
 // 180-215 TFLOP/s and took a tenth of the call.  Both are bound by memory here: 147 KB of q_abs written
-// and 256 KB of partials read per row, against 17 and 34 MFLOP.
+// and 256 KB of partials read per row, against 17 and 34 MFLOP.  For 512 rows of one chunk the absorption takes 35 us
+// (2.9 TB/s), the projection 55 (2.7 TB/s, 1.7 waves of CTAs whose stages wait for one another: barrier and memory
+// stalls even); for 128 rows of two chunks 14 and 21.
 //
 // Every wait is bounded; a wait that runs out records MLA_ERR_TIMEOUT, and the CTA still frees its tensor
 // memory.  The next kernel may launch only once a CTA holds its tensor memory: CTAs of two kernels share an
@@ -366,8 +368,8 @@ bool encode_box(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, u
 
 }  // namespace
 
-// Above 16 rows, where the mma.sync form leaves its single wave (24 rows: 48.9 us a call against 50.6; 96: 80.2
-// and 84.2; the kernel alone at 512 rows: 35 and 48).
+// Above 16 rows, where the mma.sync form leaves its single wave (24 rows: 1.7 us a call less; 96: 4; the
+// kernel alone at 512 rows: 35 and 48).
 bool absorb_tc_pays(int rows) { return rows > 16; }
 // One 16-row tile merges faster in clusters of four CTAs a head (launch_combine_mma; a window's call of 8 rows 29 us
 // against 43, of 16 rows 34 and 37).  Above that a cluster takes its rows one pass after another, and this kernel a
