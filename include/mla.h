@@ -273,10 +273,11 @@ MLA_API mla_status mla_cache_reserve(const mla_dims *dims, const int32_t *new_le
 
 /*
  * mla_cache_fork — requests dst_req[i] become copies of what requests src_req[i] were before the call
- * (device [n_fork] each): full pages are shared (page_refs counts the new holder, dropped entries stay
- * dropped), the rows of a partly filled last page are copied into a new page, so that source and copy
- * can both grow.  A source's full pages are shared with the drafted nodes in them: fork while a source
- * has none (before they are reserved, or after mla_cache_accept).  The destinations must be empty (seq_lens 0), each named once; a source may be named
+ * (device [n_fork] each): full pages are shared (page_refs counts the new holder), the rows of a partly
+ * filled last page are copied into a new page, so that source and copy can both grow, and dropped entries
+ * stay dropped.  Full pages are shared with the drafted nodes in them: fork a source while it has none
+ * (before they are reserved, or after mla_cache_accept).  The destinations must be empty (seq_lens 0),
+ * each named once; a source may be named
  * many times.  A bad index or length or a destination in use (MLA_ERR_DEVICE_BOUNDS) or too few free
  * pages (MLA_ERR_NO_PAGES) leaves everything as it was.  A page id outside the pool is reported
  * (MLA_ERR_DEVICE_BOUNDS), and its rows are not copied.
@@ -290,7 +291,8 @@ MLA_API mla_status mla_cache_fork(const mla_dims *dims, const int32_t *src_req, 
  * mla_cache_release — drops pages of requests req_idx[i] (device [n_req]): their entries become -1
  * and the pages lose a holder.  With first_page and last_page NULL a request drops all its pages and
  * its length becomes 0; otherwise (device [n_req] each) it drops the entries [first_page[i],
- * last_page[i]) that it has and keeps its length: the pages behind a sliding window, for instance.
+ * last_page[i]) that it has and keeps its length: the pages behind a sliding window, for instance (not a
+ * partly filled last page of a request that goes on growing: mla_cache_reserve only adds pages behind it).
  * An entry that is named twice is dropped once.  A request or page out of range, or a page that
  * nobody holds, is reported (MLA_ERR_DEVICE_BOUNDS) and skipped.
  */

@@ -270,9 +270,15 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__res
             if (pg >= p.n_pages) report(p.err, MLA_ERR_DEVICE_BOUNDS);
             else if (pg >= 0) atomicAdd(p.refs + pg, 1);          // a dropped page (< 0) has no holder to add
         }
-        if (rem && sets.n) {
-            const int from = *p.entry(s, full), to = *p.entry(d, full);
-            if (from < 0 || from >= p.n_pages || to < 0 || to >= p.n_pages) {
+        const int from = rem ? *p.entry(s, full) : -1, to = rem ? *p.entry(d, full) : -1;
+        if (rem && from < 0) {   // dropped in the source: so it is in the copy, and the page meant for it is free again
+            cooperative_groups::this_cluster().sync();   // every block has read the entries
+            if (rank == 0 && threadIdx.x == 0 && to >= 0 && to < p.n_pages) {
+                *p.entry(d, full) = -1;
+                p.refs[to] = 0;
+            }
+        } else if (rem && sets.n) {
+            if (from >= p.n_pages || to < 0 || to >= p.n_pages) {
                 if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
             } else {
 #pragma unroll

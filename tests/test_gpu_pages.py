@@ -474,3 +474,24 @@ def test_a_call_right_behind_one_that_changes_lengths(op, B):
         mla.mla_get_device_status()
         assert torch.equal(result, want)
     assert (p.d_refs == 0).all() and (p.d_lens == 0).all()
+
+
+@pytest.mark.parametrize("cached", [True, False])
+def test_fork_of_a_request_whose_last_page_was_dropped(cached):
+    p = Pool("dsv2", (100, 70, 0, 0, 0), 10, layers=2)
+    p.both("release", (0,), (1,), (2,))
+    lat = (p.d_lat, p.layers) if cached else (None, 1)
+    mla.mla_cache_fork(p.dims, p.i32((0, 1, 0)), p.i32((2, 3, 4)), 3, *p.tail(), lat[0], None, lat[1])
+    mla.mla_get_device_status()
+    free = p.free()
+    p.refs[p.table[0, 0]] += 2
+    p.refs[p.table[1, 0]] += 1
+    p.table[2, 0] = p.table[4, 0] = p.table[0, 0]
+    p.table[3, :2] = p.table[1, 0], free[1]                 # the second of three pages taken; the others are free again
+    p.refs[free[1]] = 1
+    p.lens[2:] = 100, 70, 100
+    if cached:
+        p.lat[:, free[1], :6] = p.lat[:, p.table[1, 1], :6]
+    else:
+        p.lat = p.d_lat.cpu()
+    p.check()
