@@ -435,7 +435,7 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
             MLA_CUDA(launch_decode_simt(d, a, st), "launch decode (CUDA cores)");
         }
         if (parts == PART_BLOCKS) {
-            MLA_CUDA(launch_project_tc(d, part_o, part_ml, row_first, L.rows, W_uv, out, err, sms, st, keep_empty),
+            MLA_CUDA(launch_project_tc(d, part_o, part_ml, row_first, L.rows, W_uv, out, err, st, keep_empty),
                      "launch merge + W_UV (tcgen05)");
         } else if (combine_mma_ok(d, L.DV, true)) {
             // The plan's row starts from the host lengths (the device plan is built from the same rule).

@@ -8,8 +8,7 @@
 // products are 128-row tiles of tcgen05.mma (one CTA, cta_group::1); on mma.sync they ran at
 // 180-215 TFLOP/s and took a tenth of the call.  Both are bound by memory here: 147 KB of q_abs written
 // and 256 KB of partials read per row, against 17 and 34 MFLOP.  For 512 rows of one chunk the absorption takes 35 us
-// (2.9 TB/s), the projection 55 (2.7 TB/s, 1.7 waves of CTAs whose stages wait for one another: barrier and memory
-// stalls even); for 128 rows of two chunks 14 and 21.
+// (3.3 TB/s), the projection 49 (3.4 TB/s); for 128 rows of two chunks 14 and 21.
 //
 // Every wait is bounded; a wait that runs out records MLA_ERR_TIMEOUT, and the CTA still frees its tensor
 // memory.  The next kernel may launch only once a CTA holds its tensor memory: CTAs of two kernels share an
@@ -167,7 +166,9 @@ __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ 
 // the rows' chunk partials of a block (a row with one chunk, the usual case, is only scaled by 1 / l) and
 // write them as two bf16 values hi + lo, K-major and swizzled as a tensor copy would, so that the product
 // sees 16 bits of the merged latent; the W_UV block comes by TMA.  One thread issues the block's eight MMAs
-// (hi and lo, M128 N128 K16) while the others merge the next one, whose partials are already in flight.
+// (hi and lo, M128 N128 K16) while the others merge the next one, whose partials are already in flight: two blocks of
+// a row's only chunk, or a block of its first two.  Those registers leave room for one CTA on an SM; with half of them
+// and two CTAs, 128 rows of two chunks took 31 us instead of 21, and calls of 128 to 300 rows 1 to 2 us more.
 constexpr uint32_t PJ_STAGE = 3 * BLK;         // hi | lo | W_UV
 constexpr uint32_t PJ_INFO = 2 * PJ_STAGE;     // int k0[128], k1[128]; float w0[128], m[128], inv[128]
 constexpr uint32_t PJ_BAR = PJ_INFO + 5 * 4 * TM;
@@ -178,10 +179,7 @@ enum { P_FULL = 0, P_EMPTY = 2, P_COUNT = 4 };
 
 constexpr int PJ_THREADS = 512;
 
-// AHEAD: a row's second chunk is fetched a block ahead like its first, in registers that leave room for one CTA
-// on an SM.
-template <bool AHEAD>
-__global__ void __launch_bounds__(PJ_THREADS, AHEAD ? 1 : 2) project_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
+__global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                             const float *__restrict__ part_o,
                                                             const float *__restrict__ part_ml,
                                                             const int *__restrict__ row_first, int rows, int H, int hpw,
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(PJ_THREADS, AHEAD ? 1 : 2) project_tc_kernel(c
         w0[i] = w0s[r];
         held |= (uint32_t)(k < k1s[r]) << i;
         w1[i] = 0.f;
-        if (AHEAD && k + 1 < k1s[r]) {
+        if (k + 1 < k1s[r]) {
             held |= 1u << (NR + i);
             const float m1 = ml[(size_t)(k + 1) * H + h].x;
             w1[i] = m1 == -INFINITY ? 0.f : expf(m1 - ms[r]) * invs[r];
@@ -242,62 +240,31 @@ __global__ void __launch_bounds__(PJ_THREADS, AHEAD ? 1 : 2) project_tc_kernel(c
     }
     const size_t step = (size_t)H * 16;   // float4s from one block of 64 columns to the next
     float4 x[NR], x1[NR];
-    auto load_first = [&](int kb) {
+    auto load = [&](float4 (&v)[NR], int e, int kb) {   // block kb of every row's chunk e, 0 or 1
 #pragma unroll
         for (int i = 0; i < NR; ++i)
-            x[i] = (held >> i) & 1u ? __ldcs(src[i] + kb * step) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-            if (AHEAD)
-                x1[i] = (held >> (NR + i)) & 1u ? __ldcs(src[i] + (KB + kb) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = (held >> (NR * e + i)) & 1u ? __ldcs(src[i] + (KB * e + kb) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    load_first(0);
     bool ok = true;
-#pragma unroll 1
-    for (int kb = 0; kb < KB; ++kb) {
+    // Block kb, whose first chunks are in v; refill() fetches what v is to hold next.
+    auto block = [&](int kb, float4 (&v)[NR], auto merge, auto refill) {
         const int st = kb & 1;
         uint8_t *hi = s.sbase + PJ_STAGE * st, *lo = hi + BLK;
         if (kb >= 2 && !tc::mbar_wait(bar(P_EMPTY + st), ((kb >> 1) - 1) & 1, WAIT_NS)) ok = false;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) x[i].x *= w0[i], x[i].y *= w0[i], x[i].z *= w0[i], x[i].w *= w0[i];
-        if (AHEAD) {
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
-                x[i].x += w1[i] * x1[i].x, x[i].y += w1[i] * x1[i].y, x[i].z += w1[i] * x1[i].z, x[i].w += w1[i] * x1[i].w;
-        }
-        // Further chunks: the e-th of every row together.
-        for (int e = AHEAD ? 2 : 1; e < most; ++e) {
-            float4 y[NR];
-            float wk[NR];
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const int r = r0 + RS * i, k = k0s[r] + e;
-                y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                wk[i] = -INFINITY;
-                if (k < k1s[r]) {
-                    wk[i] = ml[(size_t)k * H + h].x;
-                    y[i] = __ldcs(src[i] + e * (KB * step) + kb * step);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const int r = r0 + RS * i;
-                const float w = wk[i] == -INFINITY ? 0.f : expf(wk[i] - ms[r]) * invs[r];
-                x[i].x += w * y[i].x, x[i].y += w * y[i].y, x[i].z += w * y[i].z, x[i].w += w * y[i].w;
-            }
-        }
+        for (int i = 0; i < NR; ++i) v[i].x *= w0[i], v[i].y *= w0[i], v[i].z *= w0[i], v[i].w *= w0[i];
+        merge();
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const int r = r0 + RS * i;
-            const float4 v = x[i];
-            const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
-            const uint32_t l0 = pack_bf16(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xffff0000u));
-            const uint32_t l1 = pack_bf16(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xffff0000u));
+            const uint32_t h0 = pack_bf16(v[i].x, v[i].y), h1 = pack_bf16(v[i].z, v[i].w);
+            const uint32_t l0 = pack_bf16(v[i].x - __uint_as_float(h0 << 16), v[i].y - __uint_as_float(h0 & 0xffff0000u));
+            const uint32_t l1 = pack_bf16(v[i].z - __uint_as_float(h1 << 16), v[i].w - __uint_as_float(h1 & 0xffff0000u));
             const uint32_t at = 128 * r + (((c4 / 2) ^ (r & 7)) << 4) + 8 * (c4 & 1);
             *reinterpret_cast<uint2 *>(hi + at) = make_uint2(h0, h1);
             *reinterpret_cast<uint2 *>(lo + at) = make_uint2(l0, l1);
         }
-        if (kb + 1 < KB) load_first(kb + 1);
+        refill();
         tc::fence_proxy_async_smem();
         __syncthreads();
         if (tid == 0) {
@@ -320,6 +287,50 @@ __global__ void __launch_bounds__(PJ_THREADS, AHEAD ? 1 : 2) project_tc_kernel(c
             else ok = false;
         }
         __syncwarp();
+    };
+    // Chunks from the e0-th on, the e-th of every row together, into x.
+    auto merge_from = [&](int e0, int kb) {
+        for (int e = e0; e < most; ++e) {
+            float4 y[NR];
+            float wk[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int r = r0 + RS * i, k = k0s[r] + e;
+                y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                wk[i] = -INFINITY;
+                if (k < k1s[r]) {
+                    wk[i] = ml[(size_t)k * H + h].x;
+                    y[i] = __ldcs(src[i] + e * (KB * step) + kb * step);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int r = r0 + RS * i;
+                const float w = wk[i] == -INFINITY ? 0.f : expf(wk[i] - ms[r]) * invs[r];
+                x[i].x += w * y[i].x, x[i].y += w * y[i].y, x[i].z += w * y[i].z, x[i].w += w * y[i].w;
+            }
+        }
+    };
+    load(x, 0, 0);
+    if (__syncthreads_or(most > 1)) {   // two chunks of every row in flight
+        load(x1, 1, 0);
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb)
+            block(kb, x,
+                  [&] {
+#pragma unroll
+                      for (int i = 0; i < NR; ++i)
+                          x[i].x += w1[i] * x1[i].x, x[i].y += w1[i] * x1[i].y, x[i].z += w1[i] * x1[i].z, x[i].w += w1[i] * x1[i].w;
+                      merge_from(2, kb);
+                  },
+                  [&] { if (kb + 1 < KB) load(x, 0, kb + 1), load(x1, 1, kb + 1); });
+    } else {   // two blocks of every row's only chunk in flight
+        load(x1, 0, 1);
+#pragma unroll 1
+        for (int kb = 0; kb < KB; kb += 2) {
+            block(kb, x, [] {}, [&] { if (kb + 2 < KB) load(x, 0, kb + 2); });
+            block(kb + 1, x1, [] {}, [&] { if (kb + 3 < KB) load(x1, 0, kb + 3); });
+        }
     }
     if (!tc::mbar_wait(bar(P_EMPTY + 1), ((KB - 1) >> 1) & 1, WAIT_NS)) ok = false;
     if (!ok) report(err, MLA_ERR_TIMEOUT);
@@ -394,16 +405,13 @@ cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, con
 }
 
 cudaError_t launch_project_tc(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
-                              const void *W_uv, void *out, int *err, int sms, cudaStream_t st, bool keep_empty) {
+                              const void *W_uv, void *out, int *err, cudaStream_t st, bool keep_empty) {
     if (ceil_div(rows, TM) > 65535) return cudaErrorInvalidValue;
     CUtensorMap tm_w;
     if (!encode_box(&tm_w, W_uv, D_C, (uint64_t)d.n_groups() * D_V, 0)) return cudaErrorInvalidValue;
-    // With a CTA per SM or fewer, its registers may be twice as many: 128 rows of one chunk 129 -> 122 us a call, of two
-    // 170 -> 155.
-    const auto kernel = d.H * ceil_div(rows, TM) <= sms ? project_tc_kernel<true> : project_tc_kernel<false>;
-    cudaError_t e = raise_smem_limit((const void *)kernel, PJ_SMEM);
+    cudaError_t e = raise_smem_limit((const void *)project_tc_kernel, PJ_SMEM);
     if (e != cudaSuccess) return e;
-    MLA_STEP_LAUNCH(kernel, dim3(d.H, ceil_div(rows, TM)), dim3(PJ_THREADS), PJ_SMEM, st, tm_w, part_o, part_ml,
+    MLA_STEP_LAUNCH(project_tc_kernel, dim3(d.H, ceil_div(rows, TM)), dim3(PJ_THREADS), PJ_SMEM, st, tm_w, part_o, part_ml,
                     row_first, rows, d.H, d.hpw, (__nv_bfloat16 *)out, keep_empty, err);
     return cudaGetLastError();
 }

@@ -23,7 +23,7 @@ bool project_tc_pays(int rows, long long n_work);
 cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch, int s_q,
                              void *q_abs, const PlanArgs &plan, cudaStream_t st);
 cudaError_t launch_project_tc(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
-                              const void *W_uv, void *out, int *err, int sms, cudaStream_t st, bool keep_empty);
+                              const void *W_uv, void *out, int *err, cudaStream_t st, bool keep_empty);
 
 // Test hook of the bounded waits: later tcgen05 decodes on the calling thread skip the completion
 // signal of pipeline step `withhold_step` (-1: none) and give up every wait after `wait_ns`
