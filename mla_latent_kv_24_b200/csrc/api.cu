@@ -417,8 +417,7 @@ static mla_status run_decode(Path path, const mla_dims *dims, const void *q, con
             MLA_CUDA(launch_q_absorb_mma(d, q, W_uk, seq_lens, batch, s_q, qp, pa, st),
                      "launch q_absorb (tensor cores) + plan");
         } else {
-            MLA_CUDA(launch_plan(pa, st), "launch plan");
-            MLA_CUDA(launch_q_absorb(d, q, W_uk, seq_lens, batch, s_q, qp, st, hv.v), "launch q_absorb");
+            MLA_CUDA(launch_q_absorb(d, q, W_uk, seq_lens, batch, s_q, qp, pa, st), "launch q_absorb + plan");
         }
         // A view's rows are merged by the kernel that suits their number, each from its own layout.
         PartLayout parts = tc ? PART_OCTETS : PART_ROWS;

@@ -28,19 +28,15 @@ cudaError_t launch_append_mma(const Dims &d, const void *h, int hidden, const vo
                               const int *req, const int *slot, const int *pos, int n_tok, const int *page_table,
                               int batch, int max_pages, int n_pages, void *cache, int *err, cudaStream_t st);
 
-// Split plan from device seq_lens as a kernel of its own (plan.cu).  launch_q_absorb_mma and
-// launch_q_rope build the same plan in an extra block instead.
-cudaError_t launch_plan(const PlanArgs &a, cudaStream_t st);
-
 // q absorption through W_UK + RoPE of the query's RoPE part (absorb.cu):
 //   q_abs [rows, H, d_c + d_r] = [W_UK[w]^T q_nope | RoPE(q_rope, p)], rows = batch * s_q,
-// with p = L - s_q + j, or for a tree's node L - n_nodes + its depth.
+// with p = L - s_q + j, or for a tree's node L - n_nodes + its depth.  The split plan `plan` is built in
+// one extra block.
 cudaError_t launch_q_absorb(const Dims &d, const void *q, const void *W_uk, const int *seq_lens,
-                            int batch, int s_q, void *q_abs, cudaStream_t st, const View &view = View{});
+                            int batch, int s_q, void *q_abs, const PlanArgs &plan, cudaStream_t st);
 
 // Tensor-core variant for bf16, d_nope = 128, d_c = 512, d_rope = 64 (absorb.cu).
 bool q_absorb_mma_ok(const Dims &d);
-// It also builds the split plan `plan` in one extra block.
 cudaError_t launch_q_absorb_mma(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch,
                                 int s_q, void *q_abs, const PlanArgs &plan, cudaStream_t st);
 

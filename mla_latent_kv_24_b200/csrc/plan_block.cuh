@@ -5,8 +5,8 @@
 // [s_q, max_pages * page]) sets MLA_ERR_INVALID_ARG and leaves an all-empty plan, so no kernel
 // reads or writes out of range.
 //
-// The block is either a kernel of its own (plan.cu) or one extra block of the query-preparation
-// kernel that runs before the decode, which saves a launch per call.
+// The block is one extra block of the query-preparation kernel that runs before the decode, which
+// saves a launch per call.
 #pragma once
 
 #include "common.cuh"
