@@ -271,10 +271,25 @@ def mla_debug_decode_fault(withhold_step: int, wait_us: int = 0) -> None:
 # caller's structures, so their types, sizes and device are checked here: a short or narrow one
 # would be read past its end.
 # ---------------------------------------------------------------------------------------
+_torch = None   # the module, kept: an import statement costs 0.1 us of a call
+
+
 def _here() -> int:
     """The current device; one that no tensor is on while CUDA has not been used."""
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -2
+
+
+def _stream_on(stream, here) -> Optional[int]:
+    """_stream for a caller that knows the current device."""
+    if stream is None and here >= 0:
+        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(here)
+    return _stream(stream)
 
 
 def _arr(name, t, itemsize, n, here, optional=False) -> Optional[int]:
@@ -299,7 +314,10 @@ def _host_lens(name, x, n):
         np.ascontiguousarray(np.asarray(x, dtype=np.int32))
     if a.size < n:
         raise ValueError(f"{name} has {a.size} elements, expected at least {n}")
-    return a, a.ctypes.data
+    try:
+        return a, ctypes.addressof(ctypes.c_char.from_buffer(a))   # a third of the time of a.ctypes.data
+    except (TypeError, ValueError):                                # read-only, or empty
+        return a, a.ctypes.data
 
 
 def _decode_view_args(dims, q, s_q, cache, n_pages_total, batch, max_pages, page_table, seq_lens, out, here):
@@ -345,7 +363,7 @@ def mla_decode_tree(dims, q, W_uk, W_uv, latent_cache, page_table, seq_lens, n_n
                                   _arr("n_nodes", n_nodes, 4, batch, here), lp, np_,
                                   _arr("depths", depths, 4, batch * max_nodes, here),
                                   _arr("tree_mask", tree_mask, 8, batch * max_nodes, here), batch, max_nodes, max_pages,
-                                  n_pages_total, op, ws, nbytes, _stream(stream)))
+                                  n_pages_total, op, ws, nbytes, _stream_on(stream, here)))
 
 
 def mla_decode_window_workspace_size(dims, batch, s_q, sinks, window, seq_lens_host) -> int:
@@ -365,7 +383,7 @@ def mla_decode_window(dims, q, W_uk, W_uv, latent_cache, page_table, seq_lens, s
     uk, uv = _weights(dims, e, W_uk, W_uv, here)
     ws, nbytes = _workspace(workspace, workspace_bytes, here)
     _check(load().mla_decode_window(ctypes.byref(dims), qp, uk, uv, cp, tp, sp, lp, batch, s_q, sinks, window,
-                                    max_pages, n_pages_total, op, ws, nbytes, _stream(stream)))
+                                    max_pages, n_pages_total, op, ws, nbytes, _stream_on(stream, here)))
 
 
 def gqla_decode_window_workspace_size(dims, batch, s_q, sinks, window, seq_lens_host) -> int:
@@ -386,7 +404,7 @@ def gqla_decode_window(dims, q, expanded_cache, latent_cache, page_table, seq_le
     ep = _arr("expanded_cache", expanded_cache, e, n_pages_total * g * dims.page_size * (dims.d_nope + dims.d_v), here)
     ws, nbytes = _workspace(workspace, workspace_bytes, here)
     _check(load().gqla_decode_window(ctypes.byref(dims), qp, ep, cp, tp, sp, lp, batch, s_q, sinks, window, max_pages,
-                                     n_pages_total, op, ws, nbytes, _stream(stream)))
+                                     n_pages_total, op, ws, nbytes, _stream_on(stream, here)))
 
 
 def mla_cache_append_slots(dims, h, hidden, W_dkv, W_kr, req_idx, slots, positions, n_tok, page_table, batch,
@@ -399,7 +417,7 @@ def mla_cache_append_slots(dims, h, hidden, W_dkv, W_kr, req_idx, slots, positio
         _arr("W_kr", W_kr, e, dims.d_rope * hidden, here, True), _arr("req_idx", req_idx, 4, n_tok, here),
         _arr("slots", slots, 4, n_tok, here), _arr("positions", positions, 4, n_tok, here), n_tok,
         _arr("page_table", page_table, 4, batch * max_pages, here), batch, max_pages, n_pages_total,
-        _arr("latent_cache", latent_cache, e, n_pages_total * dims.page_size * row, here), _stream(stream)))
+        _arr("latent_cache", latent_cache, e, n_pages_total * dims.page_size * row, here), _stream_on(stream, here)))
 
 
 def _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here, refs_optional=False):
@@ -420,7 +438,7 @@ def mla_cache_reserve(dims, new_lens, seq_lens, page_table, batch, max_pages, pa
     here = _here()
     s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here)
     _check(load().mla_cache_reserve(ctypes.byref(dims), _arr("new_lens", new_lens, 4, batch, here), s, t, batch,
-                                    max_pages, r, n_pages_total, _stream(stream)))
+                                    max_pages, r, n_pages_total, _stream_on(stream, here)))
 
 
 def mla_cache_fork(dims, src_req, dst_req, n_fork, seq_lens, page_table, batch, max_pages, page_refs, n_pages_total,
@@ -430,7 +448,7 @@ def mla_cache_fork(dims, src_req, dst_req, n_fork, seq_lens, page_table, batch, 
     lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total, here)
     _check(load().mla_cache_fork(ctypes.byref(dims), _arr("src_req", src_req, 4, n_fork, here),
                                  _arr("dst_req", dst_req, 4, n_fork, here), n_fork, s, t, batch, max_pages, r,
-                                 n_pages_total, lat, exp, n_layers, _stream(stream)))
+                                 n_pages_total, lat, exp, n_layers, _stream_on(stream, here)))
 
 
 def mla_cache_release(dims, req_idx, first_page, last_page, n_req, seq_lens, page_table, batch, max_pages, page_refs,
@@ -440,7 +458,7 @@ def mla_cache_release(dims, req_idx, first_page, last_page, n_req, seq_lens, pag
     _check(load().mla_cache_release(ctypes.byref(dims), _arr("req_idx", req_idx, 4, n_req, here),
                                     _arr("first_page", first_page, 4, n_req, here, True),
                                     _arr("last_page", last_page, 4, n_req, here, True), n_req, s, t, batch, max_pages,
-                                    r, n_pages_total, _stream(stream)))
+                                    r, n_pages_total, _stream_on(stream, here)))
 
 
 def mla_cache_accept(dims, ctx_lens, n_nodes, accepted, n_accepted, max_nodes, seq_lens, page_table, batch, max_pages,
@@ -452,4 +470,4 @@ def mla_cache_accept(dims, ctx_lens, n_nodes, accepted, n_accepted, max_nodes, s
                                    _arr("n_nodes", n_nodes, 4, batch, here),
                                    _arr("accepted", accepted, 4, batch * max_nodes, here),
                                    _arr("n_accepted", n_accepted, 4, batch, here), max_nodes, s, t, batch, max_pages, r,
-                                   n_pages_total, lat, exp, n_layers, _stream(stream)))
+                                   n_pages_total, lat, exp, n_layers, _stream_on(stream, here)))
