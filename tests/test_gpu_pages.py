@@ -495,3 +495,60 @@ def test_fork_of_a_request_whose_last_page_was_dropped(cached):
     else:
         p.lat = p.d_lat.cpu()
     p.check()
+
+
+def status():
+    try:
+        mla.mla_get_device_status()
+    except mla.MlaError as e:
+        return e.status
+    return 0
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sequences(seed):
+    rs = np.random.RandomState(seed)
+    shape, nb = list(SHAPES)[seed % 4], int(rs.choice([1, 3, 8, 40]))
+    page = mla.make_dims(**SHAPES[shape]).page_size
+    lens = tuple(int(x) for x in rs.choice([0, 0, 1, page - 1, page, page + 1, 3 * page + 5], size=nb))
+    n_pages = max(1, sum(-(-x // page) for x in lens) + int(rs.randint(0, 6 * nb + 1)))
+    p = Pool(shape, lens, n_pages, layers=1 + seed % 2, slack=5, seed=seed, expanded=seed % 3 == 0)
+
+    def some(lo, hi, n):
+        return [int(x) for x in rs.randint(lo, hi, size=n)]
+
+    for op in rs.choice(["reserve", "fork", "release", "range", "accept", "accept"], size=12):
+        if op == "reserve":
+            new = np.minimum(p.lens + rs.choice([0, 0, 1, page, 2 * page - 1], size=nb), p.max_pages * page).astype(np.int32)
+            need, args = sum(p.pages(new[b]) - p.pages(p.lens[b]) for b in range(nb)), (new,)
+        elif op == "fork":
+            dst = [int(x) for x in rs.permutation(np.flatnonzero(p.lens == 0))][:rs.randint(1, nb + 1)]
+            if not dst:
+                continue
+            src = some(0, nb, len(dst))
+            need, args = sum(int(p.lens[s]) % page > 0 for s in src), (src, dst)
+        elif op == "release":
+            need, args = 0, (sorted(set(some(0, nb, 3))),)
+        elif op == "range":                                    # full pages, ranges that overlap or are empty
+            req = some(0, nb, 3)
+            first = some(-2, 5, 3)
+            last = [min(int(p.lens[b]) // page, a + int(rs.randint(-1, 3))) for b, a in zip(req, first)]
+            op, need, args = "release", 0, (req, first, last)
+        else:                                                  # trees in pages that their request holds alone
+            max_nodes = int(rs.choice([1, 8, 64]))
+            nodes, acc = [], []
+            for b in range(nb):
+                L, n = int(p.lens[b]), 0
+                while n < min(max_nodes, L) and p.table[b, (L - n - 1) // page] >= 0 and \
+                        p.refs[p.table[b, (L - n - 1) // page]] == 1:
+                    n += 1
+                nodes.append(int(rs.randint(0, n + 1)))
+                acc.append(sorted(int(x) for x in rs.permutation(nodes[-1])[:rs.randint(0, nodes[-1] + 1)]))
+            need, args = 0, (p.lens - np.asarray(nodes, np.int32), nodes, acc, max_nodes)
+        getattr(p, op)(*args)
+        if need > len(p.free()):
+            assert status() == 7
+        else:
+            assert status() == 0
+            getattr(p, "m_" + op)(*(args[:3] if op == "accept" else args))
+        p.check()
