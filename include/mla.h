@@ -257,8 +257,8 @@ MLA_API mla_status mla_cache_append_slots(const mla_dims *dims, const void *h, i
  * Everything is read and changed on the device: the calls need no host copy of a length and can be
  * captured into a graph.  New pages are the lowest free ids in the order of the requests (forks), so
  * results do not depend on timing.  Calls on one pool must be ordered (one stream, or events).
- * Each error below goes to the device error word; n_pages_total <= 2^30, batch and n_fork <= 8192
- * (release: any batch and n_req).
+ * Each error below goes to the device error word; n_pages_total <= 2^30, batch * max_pages < 2^31,
+ * batch and n_fork <= 8192 (release: any batch and n_req).
  */
 
 /*

@@ -801,6 +801,7 @@ static mla_status check_pool(const mla_dims *dims, int32_t *seq_lens, int32_t *p
     if (batch <= 0 || max_pages <= 0 || n_pages_total <= 0)
         return fail(MLA_ERR_INVALID_ARG, "batch, max_pages, n_pages_total must be > 0");
     if ((long long)max_pages * d->page > INT_MAX) return fail(MLA_ERR_UNSUPPORTED, "max_pages * page too large");
+    if ((long long)batch * max_pages > INT_MAX) return fail(MLA_ERR_UNSUPPORTED, "batch * max_pages too large");
     if (n_pages_total > PAGES_MAX_TOTAL) return fail(MLA_ERR_UNSUPPORTED, "n_pages_total too large");
     if (!aligned16(page_refs)) return fail(MLA_ERR_INVALID_ARG, "page_refs must be 16-byte aligned");
     *p = PagePool{seq_lens, page_table, page_refs, batch, max_pages, n_pages_total, d->page, nullptr};

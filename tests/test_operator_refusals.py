@@ -133,3 +133,13 @@ def test_binding_refuses_short_or_narrow_tensors():
         mla.mla_decode_tree(d, q, W, W, cache, i(1), i(1), i(1), [8], [4], i(4), i(4, torch.int64), 1, 4, 1, 1, out,
                             ws[:256], workspace_bytes=1 << 30)
     assert e.value.status == 3
+
+
+def test_pool_sizes_whose_page_counts_pass_31_bits():
+    # a sum over all requests' pages would wrap
+    d, lib = ctypes.byref(mla.make_dims()), mla.load()
+    for batch, max_pages in ((64, 1 << 25), (8192, 1 << 18)):
+        assert lib.mla_cache_reserve(d, P, P, P, batch, max_pages, P, 1, None) == UNSUPPORTED
+        assert lib.mla_cache_fork(d, P, P, 1, P, P, batch, max_pages, P, 1, P, None, 1, None) == UNSUPPORTED
+        assert lib.mla_cache_release(d, P, None, None, 1, P, P, batch, max_pages, P, 1, None) == UNSUPPORTED
+        assert lib.mla_cache_accept(d, P, P, P, P, 8, P, P, batch, max_pages, P, 1, P, None, 1, None) == UNSUPPORTED
