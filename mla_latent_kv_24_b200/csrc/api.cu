@@ -193,7 +193,10 @@ mla_status make_layout(const Dims &d, Path path, bool tc, int sms, int batch, in
         granule = grouped_token_granule();
     } else {
         const int hb = simt_heads_per_block(d, path == ABSORBED ? 0 : 1);
-        units = std::max(1, 4 * sms / std::max(1, d.H / hb));
+        // A view's rows are many: shorter chunks than the causal rows' (float32 trees of the tiny shape, 512 rows of 60 to
+        // 1,030 tokens: 121 us a call with 4 units per SM, 102 with 8; 16 heads in bf16: 2,467 and 1,920; 64 rows: 28
+        // and 29).
+        units = std::max(1, (hv.v.kind == VIEW_CAUSAL ? 4 : 8) * sms / std::max(1, d.H / hb));
         granule = 32;
     }
     L->plan_sq = (path == GROUPED && grouped_tc_ok(d, s_q)) ? 1 : s_q;

@@ -23,7 +23,6 @@ constexpr int TT = 32;        // tokens per tile (one per lane)
 constexpr int WARPS = 8;
 constexpr int MAX_HB = 16;    // heads per CTA
 constexpr int HPW = MAX_HB / WARPS;
-constexpr int MAX_VL = 16;    // value columns per lane (DV <= 512)
 
 struct P {
     const void *q, *latent, *expanded;
@@ -48,7 +47,9 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-template <typename T, int MODE, bool VIEW>
+// VL: value columns per lane, DV <= 32 VL.  (With sixteen for every shape, a short row's columns were mostly tests of
+// the bound: 512 tree rows of the tiny shape 347 us a call, 121 with one.)
+template <typename T, int MODE, bool VIEW, int VL>
 __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
     step_begin();
     extern __shared__ float smem[];
@@ -79,15 +80,14 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
         qs[i] = to_f32(q[((size_t)it.row * p.H + h0 + hh) * p.DK + k]);
     }
 
-    float m[HPW], l[HPW], acc[HPW][MAX_VL];
+    float m[HPW], l[HPW], acc[HPW][VL];
 #pragma unroll
     for (int i = 0; i < HPW; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int v = 0; v < MAX_VL; ++v) acc[i][v] = 0.f;
+        for (int v = 0; v < VL; ++v) acc[i][v] = 0.f;
     }
-    const int nvl = (p.DV + 31) / 32;
 
     for (int tb = it.t0; tb < it.t1; tb += TT) {
         __syncthreads();
@@ -155,13 +155,13 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
             l[i] = l[i] * alpha + warp_sum(e);
             m[i] = mnew;
 #pragma unroll
-            for (int v = 0; v < MAX_VL; ++v) acc[i][v] *= alpha;
+            for (int v = 0; v < VL; ++v) acc[i][v] *= alpha;
             for (int t = 0; t < TT; ++t) {
                 const float pt = __shfl_sync(0xffffffffu, e, t);
                 const float *vr = V + t * VST;
 #pragma unroll
-                for (int v = 0; v < MAX_VL; ++v)
-                    if (v < nvl && lane + 32 * v < p.DV) acc[i][v] += pt * vr[lane + 32 * v];
+                for (int v = 0; v < VL; ++v)
+                    if (lane + 32 * v < p.DV) acc[i][v] += pt * vr[lane + 32 * v];
             }
         }
     }
@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
         if (hh >= nh) break;
         const size_t base = (size_t)blockIdx.x * p.H + h0 + hh;
 #pragma unroll
-        for (int v = 0; v < MAX_VL; ++v)
-            if (v < nvl && lane + 32 * v < p.DV) p.part_o[base * p.DV + lane + 32 * v] = acc[i][v];
+        for (int v = 0; v < VL; ++v)
+            if (lane + 32 * v < p.DV) p.part_o[base * p.DV + lane + 32 * v] = acc[i][v];
         if (lane == 0) {
             p.part_ml[base * 2] = m[i];
             p.part_ml[base * 2 + 1] = l[i];
@@ -180,13 +180,19 @@ __global__ void __launch_bounds__(WARPS * 32) decode_simt_kernel(P p) {
     }
 }
 
-template <typename T, int MODE>
-cudaError_t launch_t(const P &p, dim3 grid, size_t smem, cudaStream_t st) {
-    auto k = p.view.kind == VIEW_CAUSAL ? decode_simt_kernel<T, MODE, false> : decode_simt_kernel<T, MODE, true>;
+template <typename T, int MODE, int VL>
+cudaError_t launch_vl(const P &p, dim3 grid, size_t smem, cudaStream_t st) {
+    auto k = p.view.kind == VIEW_CAUSAL ? decode_simt_kernel<T, MODE, false, VL> : decode_simt_kernel<T, MODE, true, VL>;
     cudaError_t e = raise_smem_limit((const void *)k, smem);
     if (e != cudaSuccess) return e;
     MLA_STEP_LAUNCH(k, dim3(grid), dim3(WARPS * 32), smem, st, p);
     return cudaGetLastError();
+}
+template <typename T, int MODE>
+cudaError_t launch_t(const P &p, dim3 grid, size_t smem, cudaStream_t st) {
+    if (p.DV <= 32) return launch_vl<T, MODE, 1>(p, grid, smem, st);
+    if (p.DV <= 128) return launch_vl<T, MODE, 4>(p, grid, smem, st);
+    return launch_vl<T, MODE, 16>(p, grid, smem, st);
 }
 
 }  // namespace
