@@ -79,21 +79,26 @@ __device__ __forceinline__ uint32_t free_bits(const int *refs, int n_pages, int 
 // first_tile: this thread's free_bits() of the first pages, which the caller loads ahead of its own chain.
 template <typename Take>
 __device__ __forceinline__ bool allocate(int *refs, int n_pages, int wanted, uint32_t first_tile, const Take &take) {
-    int have = 0;
-    for (int base = 0; base < n_pages && have < wanted; base += PT * PER) {
+    if (wanted == 0) return true;
+    int first_total;
+    const int first_rank = block_prefix(__popc(first_tile), &first_total);
+    int have = first_total;
+    for (int base = PT * PER; base < n_pages && have < wanted; base += PT * PER) {
         const int at = base + (int)threadIdx.x * PER;
-        const uint32_t m = base == 0 ? first_tile : at < n_pages ? free_bits(refs, n_pages, at) : 0u;
         int total;
-        block_prefix(__popc(m), &total);
+        block_prefix(__popc(at < n_pages ? free_bits(refs, n_pages, at) : 0u), &total);
         have += total;
     }
     if (have < wanted) return false;
     int before = 0;
     for (int base = 0; before < wanted; base += PT * PER) {
         const int at = base + (int)threadIdx.x * PER;
-        uint32_t m = base == 0 ? first_tile : at < n_pages ? free_bits(refs, n_pages, at) : 0u;
-        int total;
-        int rank = before + block_prefix(__popc(m), &total);
+        uint32_t m = first_tile;
+        int rank = first_rank, total = first_total;
+        if (base) {
+            m = at < n_pages ? free_bits(refs, n_pages, at) : 0u;
+            rank = before + block_prefix(__popc(m), &total);
+        }
         for (; m && rank < wanted; m &= m - 1, ++rank) {
             const int page = at + __ffs(m) - 1;
             refs[page] = 1;
