@@ -9,7 +9,8 @@
 //
 // One CTA handles one head and up to RB query rows, so each W_UK row is read once per RB
 // rows; every thread owns two latent columns.  The CTAs past the last head are the plan's: the first
-// builds it, which saves a launch (float32 trees of the tiny shape: 23.4 -> 21.3 us a call).
+// builds it, which saves a launch (float32 trees of the tiny shape: 23.4 -> 21.3 us a call).  Products and
+// angles are formed before the wait for the previous kernel (calls in a row: 16.9 -> 14.8).
 #include "kernels.h"
 #include "plan_block.cuh"
 #include "rope_rows.cuh"
@@ -24,7 +25,7 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
                                                        const int *__restrict__ seq_lens, int rows, int s_q,
                                                        int H, int hpw, int d_c, int d_r, int d_n, float base,
                                                        T *__restrict__ q_abs, PlanArgs plan) {
-    step_begin();
+    step_allow_next();   // loads, products and angles touch inputs only; every store waits (below)
     __shared__ float qn[RB][128];
     if (blockIdx.x == H) {
         static_assert(sizeof(qn) >= sizeof(int) * (2 * 512 + 1), "the plan's scratch");
@@ -41,6 +42,14 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
     }
     __syncthreads();
     const T *Wk = W_uk + (size_t)w * d_n * d_c;
+    // RoPE part: pair i of the query's RoPE vector turns by p * base^(-2i/d_r).
+    auto angle = [&](int i, float *cs, float *sn) {
+        const int row = row0 + i / (d_r / 2);
+        rope_cos_sin(query_pos(plan.view, seq_lens, row / s_q, row % s_q, s_q), i % (d_r / 2), d_r, base, cs, sn);
+    };
+    const int pairs = nr * (d_r / 2);
+    float cs = 0.f, sn = 0.f;
+    if ((int)threadIdx.x < pairs) angle(threadIdx.x, &cs, &sn);
     for (int c = threadIdx.x; c < d_c; c += blockDim.x) {
         float acc[RB];
 #pragma unroll
@@ -50,16 +59,15 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
 #pragma unroll
             for (int r = 0; r < RB; ++r) acc[r] += qn[r][k] * wv;
         }
+        step_wait_prev();   // q_abs is workspace the previous call's kernels may still read
         for (int r = 0; r < nr; ++r) q_abs[((size_t)(row0 + r) * H + h) * d_out + c] = from_f32<T>(acc[r]);
     }
-    // RoPE part: pair i of the query's RoPE vector turns by p * base^(-2i/d_r).
-    for (int i = threadIdx.x; i < nr * (d_r / 2); i += blockDim.x) {
-        const int r = i / (d_r / 2), pi = i % (d_r / 2);
-        const int row = row0 + r, b = row / s_q, j = row % s_q;
-        const int p = query_pos(plan.view, seq_lens, b, j, s_q);
+    step_wait_prev();
+    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+        const int r = i / (d_r / 2), pi = i % (d_r / 2), row = row0 + r;
+        if (i != (int)threadIdx.x) angle(i, &cs, &sn);
         const T *src = q + ((size_t)row * H + h) * d_qk + d_n + 2 * pi;
-        float x0 = to_f32(src[0]), x1 = to_f32(src[1]), cs, sn;
-        rope_cos_sin(p, pi, d_r, base, &cs, &sn);
+        const float x0 = to_f32(src[0]), x1 = to_f32(src[1]);
         T *dst = q_abs + ((size_t)row * H + h) * d_out + d_c + 2 * pi;
         dst[0] = from_f32<T>(x0 * cs - x1 * sn);
         dst[1] = from_f32<T>(x0 * sn + x1 * cs);
