@@ -429,7 +429,7 @@ def run_ours(a, rank, world, local_rank):
     def timed_loop(K, e2e_bufs=None, profile=False):
         """K steps on the device clock.  Without a flush the steps run back to back between two
         events, so each step's kernels chain as they do in a serving loop (programmatic launches
-        overlap a kernel's input loads with its predecessor); with a flush, or with `profile` (the
+        overlap a kernel's launch and set-up with its predecessor); with a flush, or with `profile` (the
         library's events around the main attention kernel, which break that chaining), each step
         is bracketed by its own events.  Returns (total step ms, mean kernel ms or None, wall s)."""
         per_step = flush is not None or profile

@@ -9,8 +9,10 @@
 //
 // One CTA handles one head and up to RB query rows, so each W_UK row is read once per RB
 // rows; every thread owns two latent columns.  The CTAs past the last head are the plan's: the first
-// builds it, which saves a launch (float32 trees of the tiny shape: 23.4 -> 21.3 us a call).  Products and
-// angles are formed before the wait for the previous kernel (calls in a row: 16.9 -> 14.8).
+// builds it, which saves a launch (float32 trees of the tiny shape: 23.4 -> 21.3 us a call).
+//
+// Queries, lengths and a tree's arrays may come from the kernel right before the call, so they are read
+// after the wait for it; what W_UK's lines need from HBM is fetched into L2 meanwhile.
 #include "kernels.h"
 #include "plan_block.cuh"
 #include "rope_rows.cuh"
@@ -21,11 +23,14 @@ namespace {
 constexpr int RB = 16;
 
 template <typename T>
-__global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, const T *__restrict__ W_uk,
-                                                       const int *__restrict__ seq_lens, int rows, int s_q,
+__global__ void __launch_bounds__(256) q_absorb_kernel(const T *q, const T *W_uk, const int *seq_lens, int rows, int s_q,
                                                        int H, int hpw, int d_c, int d_r, int d_n, float base,
                                                        T *__restrict__ q_abs, PlanArgs plan) {
-    step_allow_next();   // loads, products and angles touch inputs only; every store waits (below)
+    step_allow_next();
+    if (blockIdx.x < H && blockIdx.y == 0 && (int)threadIdx.x < d_n)   // d_c is a multiple of 8
+        prefetch_l2(W_uk + ((size_t)(blockIdx.x / hpw) * d_n + threadIdx.x) * d_c, d_c * (uint32_t)sizeof(T));
+    const double theta = rope_theta(threadIdx.x % (d_r / 2), d_r, base);   // of this thread's first pair
+    step_wait_prev();
     __shared__ float qn[RB][128];
     if (blockIdx.x == H) {
         static_assert(sizeof(qn) >= sizeof(int) * (2 * 512 + 1), "the plan's scratch");
@@ -45,7 +50,8 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
     // RoPE part: pair i of the query's RoPE vector turns by p * base^(-2i/d_r).
     auto angle = [&](int i, float *cs, float *sn) {
         const int row = row0 + i / (d_r / 2);
-        rope_cos_sin(query_pos(plan.view, seq_lens, row / s_q, row % s_q, s_q), i % (d_r / 2), d_r, base, cs, sn);
+        rope_cos_sin(query_pos(plan.view, seq_lens, row / s_q, row % s_q, s_q),
+                     i < (int)blockDim.x ? theta : rope_theta(i % (d_r / 2), d_r, base), cs, sn);
     };
     const int pairs = nr * (d_r / 2);
     float cs = 0.f, sn = 0.f;
@@ -59,10 +65,8 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
 #pragma unroll
             for (int r = 0; r < RB; ++r) acc[r] += qn[r][k] * wv;
         }
-        step_wait_prev();   // q_abs is workspace the previous call's kernels may still read
         for (int r = 0; r < nr; ++r) q_abs[((size_t)(row0 + r) * H + h) * d_out + c] = from_f32<T>(acc[r]);
     }
-    step_wait_prev();
     for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
         const int r = i / (d_r / 2), pi = i % (d_r / 2), row = row0 + r;
         if (i != (int)threadIdx.x) angle(i, &cs, &sn);
@@ -77,15 +81,15 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *__restrict__ q, 
 // GQA path: the no-position part is used as is; only the RoPE part turns.  A warp takes RH heads of a
 // row: each lane forms one pair's angle, sine and cosine (in double) once for all of them.  (One angle
 // per head and pair took 16 us for 64 rows, this 11; RH = 1, 2, 4, 8 come within 1 us of a call.)
-// Angles are formed while the previous call's merge drains (4 requests, calls in a row: 21.4 -> 20.3 us each).
 // The last block builds the split plan instead.
 constexpr int RH = 2;
 
 template <typename T>
-__global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, const int *__restrict__ seq_lens,
-                                                     int rows, int s_q, int H, int d_r, int d_n, float base,
-                                                     T *__restrict__ q_rot, PlanArgs plan) {
-    step_allow_next();   // loads and angles touch inputs only; every store waits (below)
+__global__ void __launch_bounds__(256) q_rope_kernel(const T *q, const int *seq_lens, int rows, int s_q, int H,
+                                                     int d_r, int d_n, float base, T *__restrict__ q_rot, PlanArgs plan) {
+    step_allow_next();
+    const double theta = rope_theta(threadIdx.x % 32, d_r, base);   // of the lane's pair
+    step_wait_prev();
     if (blockIdx.x == gridDim.x - 1) {
         __shared__ int scratch[2 * 512 + 1];
         plan_block<256>(plan, scratch, 512);
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, co
     const int quads = d_n * (int)sizeof(T) / 16;   // 16-byte pieces of a head's no-position part
     for (long long u = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; u < n; u += stride) {
         const int row = (int)(u / groups), h0 = (int)(u % groups) * RH, nh = min(H - h0, RH);
-        const int b = row / s_q, j = row % s_q, p = load_len(seq_lens + b) - s_q + j;
+        const int b = row / s_q, j = row % s_q, p = seq_lens[b] - s_q + j;
         const T *src = q + ((size_t)row * H + h0) * d_qk;
         T *dst = q_rot + ((size_t)row * H + h0) * d_qk;
         const bool turns = 2 * lane < d_r;
@@ -114,8 +118,7 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, co
             if (turns && h < nh) x[h] = *reinterpret_cast<const Pair *>(src + (size_t)h * d_qk + d_n + 2 * lane);
         if (lane < nh * quads) first = *piece(src, lane);
         float cs = 0.f, sn = 0.f;
-        if (turns) rope_cos_sin(p, lane, d_r, base, &cs, &sn);
-        step_wait_prev();   // q_rot is workspace the previous call's kernels may still read
+        if (turns) rope_cos_sin(p, theta, &cs, &sn);
         if (lane < nh * quads) *piece(dst, lane) = first;
 #pragma unroll 4
         for (int i = lane + 32; i < nh * quads; i += 32) *piece(dst, i) = *piece(src, i);
@@ -127,7 +130,6 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *__restrict__ q, co
                     Pair{from_f32<T>(x0 * cs - x1 * sn), from_f32<T>(x0 * sn + x1 * cs)};
             }
     }
-    step_wait_prev();   // of warps without a row: the kernel ends after its predecessor
 }
 
 }  // namespace
@@ -171,9 +173,8 @@ cudaError_t launch_q_rope(const Dims &d, const void *q, const int *seq_lens, int
 // for many it is the 147 KB written per row.
 //
 // Two forms.  Up to 16 rows one CTA computes 16 rows x 128 columns of one head, so that a decode step's
-// whole grid (4 column tiles per head) is one wave of CTAs: a CTA stores only after the previous kernel
-// has completed, and a second wave would start its loads only then.  More rows: a CTA keeps its W_UK
-// tile (128 columns) and walks 64-row tiles of the batch, the next tile's queries arriving while this
+// whole grid (4 column tiles per head) is one wave of CTAs, which waits for the previous kernel together while
+// its W_UK tiles come into L2.  More rows: a CTA keeps its W_UK tile (128 columns) and walks 64-row tiles of the batch, the next tile's queries arriving while this
 // one is multiplied, and stores whole 256-byte row pieces through shared memory.  (With 64 x 64 tiles
 // of their own, 4-byte stores and an angle per head: 82 us for 512 rows, 29 for 128; now 48 and 19.)
 //
@@ -219,6 +220,10 @@ __device__ __forceinline__ void absorb_load_w(__nv_bfloat16 *Bs, const __nv_bflo
         cp_async16(Bs + k * AB_LDB + n, Wk + (size_t)k * D_C + n0 + n, true);
     }
 }
+// The same tile into L2, ahead of the wait: one thread a row.
+__device__ __forceinline__ void absorb_prefetch_w(const __nv_bfloat16 *Wk, int n0) {
+    if (threadIdx.x < AB_K) prefetch_l2(Wk + (size_t)threadIdx.x * D_C + n0, AB_N * (uint32_t)sizeof(*Wk));
+}
 template <int TM>
 __device__ __forceinline__ void absorb_load_q(__nv_bfloat16 *As, const __nv_bfloat16 *q, int row0, int rows, int H, int h) {
     for (int c = threadIdx.x; c < TM * AB_K / 8; c += 256) {
@@ -228,21 +233,23 @@ __device__ __forceinline__ void absorb_load_q(__nv_bfloat16 *As, const __nv_bflo
 }
 
 // Up to 16 rows: grid (H + extra, 4).
-__global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *__restrict__ q,
-                                                           const __nv_bfloat16 *__restrict__ W_uk,
-                                                           const int *__restrict__ seq_lens, int rows, int s_q,
-                                                           int H, int hpw, float base,
-                                                           __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
-    step_allow_next();   // loads and products touch inputs only; every store waits (below)
+__global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *W_uk,
+                                                           const int *seq_lens, int rows, int s_q, int H, int hpw,
+                                                           float base, __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
+    step_allow_next();
     __shared__ __align__(16) __nv_bfloat16 As[16 * AB_LD];          // [rows][128 k]
     __shared__ __align__(16) __nv_bfloat16 Bs[AB_K * AB_LDB];       // [128 k][128 n]
     const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
-    if (h >= H) {
+    const __nv_bfloat16 *Wk = W_uk + (size_t)(h / hpw) * D_N * D_C;
+    if (h < H) {
+        absorb_prefetch_w(Wk, n0);
+        step_wait_prev();
+    } else {
         rope_or_plan_block((h - H) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base, q_abs, plan,
                            reinterpret_cast<int *>(Bs), ((int)sizeof(Bs) / 4 - 1) / 2);
         return;
     }
-    absorb_load_w(Bs, W_uk + (size_t)(h / hpw) * D_N * D_C, n0);
+    absorb_load_w(Bs, Wk, n0);
     absorb_load_q<16>(As, q, 0, rows, H, h);
     cp_async_commit();
     cp_async_wait<0>();
@@ -251,7 +258,6 @@ __global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *
     float acc[2][4];
     absorb_mma<2>(acc, As, Bs, 0, 16 * warp, lane);
     const int gid = lane / 4, t4 = lane % 4;
-    step_wait_prev();   // q_abs is workspace the previous call's kernels may still read
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
         const int row = gid + 8 * hr;
@@ -267,24 +273,27 @@ __global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *
 constexpr int ABR = 64;
 constexpr size_t AB_ROWS_SMEM = sizeof(__nv_bfloat16) * (AB_K * AB_LDB + 2 * ABR * AB_LD);
 
-__global__ void __launch_bounds__(256, 3) q_absorb_rows_kernel(const __nv_bfloat16 *__restrict__ q,
-                                                               const __nv_bfloat16 *__restrict__ W_uk,
-                                                               const int *__restrict__ seq_lens, int rows, int s_q,
-                                                               int H, int hpw, float base,
-                                                               __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
+__global__ void __launch_bounds__(256, 3) q_absorb_rows_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *W_uk,
+                                                               const int *seq_lens, int rows, int s_q, int H, int hpw,
+                                                               float base, __nv_bfloat16 *__restrict__ q_abs,
+                                                               PlanArgs plan) {
     step_allow_next();
     extern __shared__ __align__(16) uint8_t absm[];
     __nv_bfloat16 *Bs = reinterpret_cast<__nv_bfloat16 *>(absm);    // [128 k][128 n]
     __nv_bfloat16 *As = Bs + AB_K * AB_LDB;                         // [2][64 rows][128 k]; a tile's output too
     const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
-    if (h >= H) {
+    const __nv_bfloat16 *Wk = W_uk + (size_t)(h / hpw) * D_N * D_C;
+    if (h < H) {
+        absorb_prefetch_w(Wk, n0);
+        step_wait_prev();
+    } else {
         rope_or_plan_block(((h - H) * gridDim.z + blockIdx.z) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base,
                            q_abs, plan, reinterpret_cast<int *>(Bs), (AB_K * AB_LDB / 2 - 1) / 2);
         return;
     }
     const int tiles = ceil_div(rows, ABR), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int gid = lane / 4, t4 = lane % 4, m0 = 16 * (warp % 4), c0 = 64 * (warp / 4);
-    absorb_load_w(Bs, W_uk + (size_t)(h / hpw) * D_N * D_C, n0);
+    absorb_load_w(Bs, Wk, n0);
     absorb_load_q<ABR>(As, q, blockIdx.z * ABR, rows, H, h);
     cp_async_commit();
     int buf = 0;
@@ -308,7 +317,6 @@ __global__ void __launch_bounds__(256, 3) q_absorb_rows_kernel(const __nv_bfloat
                 *reinterpret_cast<uint32_t *>(A + (m0 + gid + 8 * hr) * AB_LD + c0 + 8 * j + 2 * t4) =
                     pack_bf16(acc[j][2 * hr], acc[j][2 * hr + 1]);
         __syncthreads();
-        step_wait_prev();   // q_abs is workspace the previous call's kernels may still read
         for (int c = threadIdx.x; c < ABR * AB_N / 8; c += 256) {
             const int r = c / (AB_N / 8), n = (c % (AB_N / 8)) * 8, row = t * ABR + r;
             if (row < rows)

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256) append_kernel(
         float x0 = acc[2 * half], x1 = acc[2 * half + 1];
         if (c >= d_c) {  // RoPE on the interleaved pair (c - d_c, c - d_c + 1)
             float cs, sn;
-            rope_cos_sin(p, (c - d_c) / 2, d_r, base, &cs, &sn);
+            rope_cos_sin(p, rope_theta((c - d_c) / 2, d_r, base), &cs, &sn);
             float y0 = x0 * cs - x1 * sn, y1 = x0 * sn + x1 * cs;
             x0 = y0;
             x1 = y1;
@@ -132,11 +132,10 @@ namespace {
 constexpr int AP_SPLIT = 8, AP_COLS = 32, AP_TOK = 16, AP_TILES = 576 / AP_COLS;
 
 __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
-    append_mma_kernel(const __nv_bfloat16 *__restrict__ h, int hidden, const __nv_bfloat16 *__restrict__ W_dkv,
-                      const __nv_bfloat16 *__restrict__ W_kr, const int *__restrict__ req,
-                      const int *__restrict__ slot, const int *__restrict__ pos, int n_tok, const int *__restrict__ page_table, int batch,
-                      int max_pages, int n_pages, float base, __nv_bfloat16 *__restrict__ cache, int *err) {
-    step_allow_next();   // loads and products touch inputs only; the cache stores wait (below)
+    append_mma_kernel(const __nv_bfloat16 *h, int hidden, const __nv_bfloat16 *W_dkv, const __nv_bfloat16 *W_kr,
+                      const int *req, const int *slot, const int *pos, int n_tok, const int *page_table, int batch,
+                      int max_pages, int n_pages, float base, __nv_bfloat16 *cache, int *err) {
+    step_allow_next();
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     constexpr int D_C = 512, D_R = 64, D_ROW = 576;
@@ -150,16 +149,39 @@ __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
     const int ct = blockIdx.x / AP_SPLIT, c0 = ct * AP_COLS, k0 = rank * ks;
     const int t0 = blockIdx.y * AP_TOK;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    auto weights = [&](int r) {   // row r of the CTA's slice
+        const int col = c0 + r;
+        return (col < D_C ? W_dkv + (size_t)col * hidden : W_kr + (size_t)(col - D_C) * hidden) + k0;
+    };
+    if (tid < AP_COLS) prefetch_l2(weights(tid), ks * (uint32_t)sizeof(*h));   // ks is a multiple of 32
+    // Rank 0's thread stores columns col, col + 1 of token n; its place and angle are found while the tiles arrive.
+    static_assert(AP_TOK * AP_COLS / 2 == 256, "a pair of columns per thread");
+    const int row = tid / (AP_COLS / 2), n = t0 + row, col = c0 + 2 * (tid % (AP_COLS / 2));
+    const bool stores = rank == 0 && n < n_tok;
+    double theta = 0.0;
+    if (stores && col >= D_C) theta = rope_theta((col - D_C) / 2, D_R, base);
+    step_wait_prev();   // hidden states and indices may come from the kernel before
+    int req_n = -1, pos_n = 0, slot_n = 0;
+    if (stores) req_n = req[n], pos_n = pos[n], slot_n = slot[n];
     for (int c = tid; c < AP_COLS * ks / 8; c += 256) {
-        const int r = c / (ks / 8), k = (c % (ks / 8)) * 8, col = c0 + r;
-        const __nv_bfloat16 *src = col < D_C ? W_dkv + (size_t)col * hidden : W_kr + (size_t)(col - D_C) * hidden;
-        cp_async16(Ws + r * ld + k, src + k0 + k, true);
+        const int r = c / (ks / 8), k = (c % (ks / 8)) * 8;
+        cp_async16(Ws + r * ld + k, weights(r) + k, true);
     }
     for (int c = tid; c < AP_TOK * ks / 8; c += 256) {
         const int r = c / (ks / 8), k = (c % (ks / 8)) * 8, tok = t0 + r;
         cp_async16(Hs + r * ld + k, h + (size_t)(tok < n_tok ? tok : 0) * hidden + k0 + k, tok < n_tok);
     }
     cp_async_commit();
+    __nv_bfloat16 *dst = nullptr;
+    float cs = 1.f, sn = 0.f;
+    if (stores) {
+        int pid = -1;
+        if (req_n >= 0 && req_n < batch && slot_n >= 0 && slot_n < max_pages * 64)
+            pid = page_table[(size_t)req_n * max_pages + slot_n / 64];
+        if (pid < 0 || pid >= n_pages) report(err, MLA_ERR_DEVICE_BOUNDS);
+        else dst = cache + ((size_t)pid * 64 + slot_n % 64) * D_ROW + col;
+        if (col >= D_C) rope_cos_sin(pos_n, theta, &cs, &sn);
+    }
     cp_async_wait<0>();
     __syncthreads();
     // warp w: tokens 0..15 x columns [8 (w % 4), 8 (w % 4) + 8), 32-wide steps w / 4, w / 4 + 2, ...
@@ -181,43 +203,24 @@ __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
     pq[(gid + 8) * AP_COLS + 8 * wc + 2 * t4] = acc[2];
     pq[(gid + 8) * AP_COLS + 8 * wc + 2 * t4 + 1] = acc[3];
     cluster.sync();
-    if (rank == 0) {
-        step_wait_prev();
-        for (int pi = tid; pi < AP_TOK * AP_COLS / 2; pi += 256) {
-            const int r = pi / (AP_COLS / 2), cp = pi % (AP_COLS / 2);
-            const int n = t0 + r, col = c0 + 2 * cp;
-            if (n >= n_tok) continue;
-            float x0 = 0.f, x1 = 0.f;
+    if (dst) {
+        float x0 = 0.f, x1 = 0.f;
 #pragma unroll
-            for (int q = 0; q < AP_SPLIT; ++q) {
-                const float *rp = cluster.map_shared_rank(part, q);
+        for (int q = 0; q < AP_SPLIT; ++q) {
+            const float *rp = cluster.map_shared_rank(part, q);
 #pragma unroll
-                for (int hq = 0; hq < 2; ++hq) {
-                    const float2 x = *reinterpret_cast<const float2 *>(rp + (hq * AP_TOK + r) * AP_COLS + 2 * cp);
-                    x0 += x.x;
-                    x1 += x.y;
-                }
+            for (int hq = 0; hq < 2; ++hq) {
+                const float2 x = *reinterpret_cast<const float2 *>(rp + (hq * AP_TOK + row) * AP_COLS + col - c0);
+                x0 += x.x;
+                x1 += x.y;
             }
-            const int b = req[n], p = pos[n], t = slot[n];
-            if (b < 0 || b >= batch || t < 0 || t >= max_pages * 64) {
-                report(err, MLA_ERR_DEVICE_BOUNDS);
-                continue;
-            }
-            const int pid = page_table[(size_t)b * max_pages + t / 64];
-            if (pid < 0 || pid >= n_pages) {
-                report(err, MLA_ERR_DEVICE_BOUNDS);
-                continue;
-            }
-            if (col >= D_C) {
-                float cs, sn;
-                rope_cos_sin(p, (col - D_C) / 2, D_R, base, &cs, &sn);
-                const float y0 = x0 * cs - x1 * sn, y1 = x0 * sn + x1 * cs;
-                x0 = y0;
-                x1 = y1;
-            }
-            __nv_bfloat16 *dst = cache + ((size_t)pid * 64 + t % 64) * D_ROW + col;
-            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(x0, x1);
         }
+        if (col >= D_C) {
+            const float y0 = x0 * cs - x1 * sn, y1 = x0 * sn + x1 * cs;
+            x0 = y0;
+            x1 = y1;
+        }
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16(x0, x1);
     }
     cluster.sync();   // partner tiles stay alive until rank 0 has read them
 }

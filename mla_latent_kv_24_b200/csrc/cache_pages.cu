@@ -7,10 +7,6 @@
 // it takes (4 bytes a page: 40,000 pages are 160 KB); one block does it, 16,384 pages at a time.
 //
 // Rows of the caches are copied with 16-byte accesses (2 or 4 bytes where a row's size asks for it).
-// These kernels write lengths and page-table entries, which the kernels of the next call may read as
-// inputs before they wait for their predecessor.  So none but the fork's first lets its successor
-// launch before all its blocks have ended, and each makes its writes visible to the device first.
-//
 // All of it is bound by launches and latency, except forks over many layers, which are bound by the
 // copied bytes.
 #include <cooperative_groups.h>
@@ -130,7 +126,7 @@ __device__ __forceinline__ uint32_t first_bits(const Pool &p) {
 
 // ------------------------------------------------------------------------------------- reserve
 __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restrict__ new_lens) {
-    step_wait_prev();
+    step_begin();
     __shared__ int off[CAP + 1];
     const uint32_t tile = first_bits(p);
     const int per = ceil_div(p.batch, PT), b0 = min(p.batch, (int)threadIdx.x * per), b1 = min(p.batch, b0 + per);
@@ -174,7 +170,6 @@ __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restri
     }
     __syncthreads();   // the lengths are read above
     for (int b = b0; b < b1; ++b) p.seq_lens[b] = new_lens[b];
-    __threadfence();
 }
 
 // ------------------------------------------------------------------------------------- fork
@@ -259,7 +254,7 @@ __device__ __forceinline__ void copy_span(char *dst, const char *src, size_t byt
 // fewer pieces than blocks.
 __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
                                                         RowSets sets) {
-    step_wait_prev();
+    step_begin();
     const int rank = blockIdx.x, blocks = gridDim.x;              // the cluster spans the grid's x
     const int s = src[blockIdx.y], d = dst[blockIdx.y];
     int L = -1;   // < 0: refused as a whole
@@ -309,7 +304,6 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__res
     }
     cooperative_groups::this_cluster().sync();   // every block has read the length's marker
     if (rank == 0 && threadIdx.x == 0 && L >= 0) p.seq_lens[d] = L;
-    __threadfence();
 }
 
 // ------------------------------------------------------------------------------------- release
@@ -329,7 +323,7 @@ __device__ __forceinline__ void drop_entry(const Pool &p, int *entry) {
 
 __global__ void __launch_bounds__(256) release_kernel(Pool p, const int *__restrict__ req, const int *__restrict__ first,
                                                       const int *__restrict__ last) {
-    step_wait_prev();
+    step_begin();
     const int b = req[blockIdx.x];
     if (b < 0 || b >= p.batch) {
         if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
@@ -350,7 +344,6 @@ __global__ void __launch_bounds__(256) release_kernel(Pool p, const int *__restr
         __syncthreads();
         if (threadIdx.x == 0) p.seq_lens[b] = 0;
     }
-    __threadfence();
 }
 
 // ------------------------------------------------------------------------------------- accept
@@ -406,7 +399,7 @@ constexpr int ACCEPT_THREADS = 288;   // 8 x 288 columns: the latent rows of 32 
 __global__ void __launch_bounds__(ACCEPT_THREADS, 4) accept_kernel(Pool p, const int *__restrict__ ctx_lens,
                                                      const int *__restrict__ n_nodes, const int *__restrict__ accepted,
                                                      const int *__restrict__ n_accepted, int max_nodes, RowSets sets) {
-    step_wait_prev();
+    step_begin();
     const int rank = blockIdx.x, blocks = gridDim.x, b = blockIdx.y;
     const int ctx = ctx_lens[b], n = n_nodes[b], n_acc = n_accepted[b];
     const int *acc = accepted + (size_t)b * max_nodes;
@@ -446,7 +439,6 @@ __global__ void __launch_bounds__(ACCEPT_THREADS, 4) accept_kernel(Pool p, const
         for (int k = p.pages_of(ctx + n_acc) + (int)threadIdx.x; k < p.pages_of(L); k += blockDim.x)
             drop_entry(p, p.entry(b, k));
     if (threadIdx.x == 0) p.seq_lens[b] = ctx + n_acc;
-    __threadfence();
 }
 
 Pool pool_of(const PagePool &a) {

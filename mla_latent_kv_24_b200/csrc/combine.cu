@@ -280,9 +280,8 @@ template <bool OCT, bool FINE, int CM>
 __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
     combine_split_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ml,
                          const int *__restrict__ row_first, const RowStarts rs, int rows, int H,
-                         const __nv_bfloat16 *__restrict__ W_uv, int hpw, __nv_bfloat16 *__restrict__ out,
-                         bool keep_empty) {
-    step_allow_next();   // the W_UV slice (an input) streams in while the decode finishes
+                         const __nv_bfloat16 *W_uv, int hpw, __nv_bfloat16 *__restrict__ out, bool keep_empty) {
+    step_allow_next();
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) uint8_t xsm[];
@@ -293,6 +292,7 @@ __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
     const int h = blockIdx.y, row0 = blockIdx.z * CM, nr = min(CM, rows - row0);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const __nv_bfloat16 *W = W_uv + (size_t)(h / hpw) * CN * CK;
+    // The W_UV slice streams in while the decode finishes: the decode has waited for all before the call.
     for (int c = tid; c < CN * XC / 8; c += 256) {   // 2048 chunks of 16 B
         const int v = c / (XC / 8), k = (c % (XC / 8)) * 8;
         cp_async16(Ws + v * X_LD + k, W + (size_t)v * CK + c0 + k, true);

@@ -601,7 +601,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                      const __grid_constant__ CUtensorMap tm_v, TcParams p) {
     // Barrier set-up and the tensor-memory allocation touch no global memory: they run while the
     // previous kernel (the query absorption) finishes; the roles start after step_wait_prev().
-    step_allow_next();
     extern __shared__ uint8_t smem_raw[];
     Ctx c;
     const uint32_t raw = tc::smem_addr(smem_raw);
@@ -657,6 +656,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc::fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(c.sbase + OFF_TMEMPTR);
     step_wait_prev();   // q_abs and the plan come from the previous kernel
+    step_allow_next();  // not before: the merge then knows that the call's inputs are complete (common.cuh)
 
     const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
     if (warp == W_KPROD) {

@@ -97,10 +97,9 @@ constexpr uint32_t AB_IDESC = tc::idesc_bf16_f32(TM, 256, false, true);
 
 __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                         const __grid_constant__ CUtensorMap tm_w,
-                                                        const __nv_bfloat16 *__restrict__ q,
-                                                        const int *__restrict__ seq_lens, int rows, int s_q, int H,
-                                                        int hpw, float base, __nv_bfloat16 *__restrict__ q_abs,
-                                                        PlanArgs plan) {
+                                                        const __nv_bfloat16 *q, const __nv_bfloat16 *W_uk,
+                                                        const int *seq_lens, int rows, int s_q, int H, int hpw,
+                                                        float base, __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
     extern __shared__ uint8_t hsm[];
     const int h = blockIdx.x, n0 = blockIdx.y * 256, row0 = blockIdx.z * TM;
     if (h >= H) {
@@ -111,6 +110,9 @@ __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ 
     }
     const Setup s = set_up<2>(hsm, AB_BAR, 256);
     step_allow_next();
+    if (row0 == 0 && threadIdx.x < D_N)
+        prefetch_l2(W_uk + ((size_t)(h / hpw) * D_N + threadIdx.x) * D_C + n0, 256 * (uint32_t)sizeof(*W_uk));
+    step_wait_prev();   // queries may come from the kernel before, and q_abs is workspace that it may still read
     const uint32_t full = s.base + AB_BAR, done = full + 8;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
@@ -152,7 +154,6 @@ __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ 
         tc::fence_after_sync();
         tmem_free(s.tmem, 256);
     }
-    step_wait_prev();   // q_abs is workspace the previous call's kernels may still read
     for (int i = warp; i < TM; i += 8) {
         const int row = row0 + i;
         if (row < rows)
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
         tc::mbar_arrive_expect_tx(bar(P_FULL + (kb & 1)), BLK);
         tma_load_2d(s.base + PJ_STAGE * (kb & 1) + 2 * BLK, &tm_w, 64 * kb, (h / hpw) * D_V, bar(P_FULL + (kb & 1)));
     };
-    if (tid == 128) load_w(0), load_w(1);   // an input: streams in while the decode finishes
+    if (tid == 128) load_w(0), load_w(1);   // streams in while the decode finishes, which has waited for all before the call
     int *k0s = reinterpret_cast<int *>(s.sbase + PJ_INFO), *k1s = k0s + TM;
     float *w0s = reinterpret_cast<float *>(k1s + TM), *ms = w0s + TM, *invs = ms + TM;
     const float2 *ml = reinterpret_cast<const float2 *>(part_ml);
@@ -399,8 +400,8 @@ cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, con
     dim3 grid(d.H + (unsigned)((rope_blocks(rows) + per) / per), 2, z);   // + the plan's and the RoPE blocks
     cudaError_t e = raise_smem_limit((const void *)absorb_tc_kernel, AB_SMEM);
     if (e != cudaSuccess) return e;
-    MLA_STEP_LAUNCH(absorb_tc_kernel, grid, dim3(256), AB_SMEM, st, tm_q, tm_w, (const __nv_bfloat16 *)q, seq_lens, rows, s_q,
-                    d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs, plan);
+    MLA_STEP_LAUNCH(absorb_tc_kernel, grid, dim3(256), AB_SMEM, st, tm_q, tm_w, (const __nv_bfloat16 *)q,
+                    (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs, plan);
     return cudaGetLastError();
 }
 

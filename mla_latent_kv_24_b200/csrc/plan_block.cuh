@@ -16,7 +16,7 @@ namespace mla {
 // Tokens of plan row r: a causal row's visible ones, or the window's or tree's virtual length
 // (view.cuh), negative for lengths that cannot be.
 __device__ __forceinline__ int plan_row_len(const PlanArgs &a, int r) {
-    const int b = r / a.s_q, j = r % a.s_q, L = load_len(a.seq_lens + b);
+    const int b = r / a.s_q, j = r % a.s_q, L = a.seq_lens[b];
     if (a.view.kind == VIEW_CAUSAL) return L - a.s_q + j + 1;
     return view_row_len(a.view.kind, a.view.sinks, a.view.window, L, a.view.kind == VIEW_TREE ? a.view.n_nodes[b] : 0,
                         a.s_q, a.n_q, j, a.page, a.max_pages * a.page);
@@ -26,7 +26,7 @@ __device__ __forceinline__ int plan_row_len(const PlanArgs &a, int r) {
 // buffers, which the plan block does not otherwise use): batches of at most cap_rows rows keep
 // the row starts and lengths there, so the block's dependent reads (the binary searches of the
 // items) never wait on global memory.  Larger batches read them back from global memory.
-// Run by all PT threads of one block (PT a multiple of 32, at most 1024).
+// Run by all PT threads of one block (PT a multiple of 32, at most 1024), after step_wait_prev().
 template <int PT>
 __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int cap_rows) {
     static_assert(PT % 32 == 0 && PT <= 1024, "one warp scans the warp totals");
@@ -42,7 +42,7 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
     __syncthreads();
     int local = 0;
     for (int r = r0; r < r1; ++r) {
-        const int L = load_len(a.seq_lens + r / a.s_q);
+        const int L = a.seq_lens[r / a.s_q];
         const int len = plan_row_len(a, r);
         if (a.view.kind == VIEW_CAUSAL ? L < a.s_q || L > a.max_pages * a.page : len < 0) atomicOr(&bad, 1);
         if (in_smem) s_len[r] = len;
@@ -70,7 +70,6 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
     }
     __syncthreads();
     const int first = warp_sum[warp] + incl - local;
-    step_wait_prev();   // a no-op once the kernel waited; else the plan is workspace the previous call may still read
     if (bad) {
         if (threadIdx.x == 0) report(a.err, MLA_ERR_INVALID_ARG);
         for (int i = threadIdx.x; i < a.n_expected; i += PT) a.items[i] = WorkItem{0, 0, 0, 0};

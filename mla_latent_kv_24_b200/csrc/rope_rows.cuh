@@ -10,8 +10,8 @@ namespace mla {
 // Position of query j of request b: the s_q queries are the request's last tokens, and a tree's
 // node sits at its depth behind the context.
 __device__ __forceinline__ int query_pos(const View &v, const int *seq_lens, int b, int j, int s_q) {
-    if (v.kind == VIEW_TREE) return load_len(seq_lens + b) - v.n_nodes[b] + v.depths[(size_t)b * s_q + j];
-    return load_len(seq_lens + b) - s_q + j;
+    if (v.kind == VIEW_TREE) return seq_lens[b] - v.n_nodes[b] + v.depths[(size_t)b * s_q + j];
+    return seq_lens[b] - s_q + j;
 }
 
 constexpr int ROPE_D_QK = 192, ROPE_D_OUT = 576;
@@ -24,21 +24,19 @@ __host__ __device__ __forceinline__ int rope_blocks(int rows) { return ceil_div(
 // A block past the heads' ones, `id` counting them: the first builds the split plan, the next
 // rope_blocks(rows) turn the RoPE part of the queries.  A warp takes every rope_warps()-th head of a row, so
 // that each pair's double-precision angle is formed once for 16 heads and more.  256 threads; `scratch`
-// has 2 cap + 1 ints.
-__device__ __forceinline__ void rope_or_plan_block(int id, const __nv_bfloat16 *__restrict__ q,
-                                                   const int *__restrict__ seq_lens, int rows, int s_q, int H, float base,
-                                                   __nv_bfloat16 *__restrict__ q_abs, const PlanArgs &plan, int *scratch,
-                                                   int cap) {
+// has 2 cap + 1 ints.  Waits for the previous kernel.
+__device__ __forceinline__ void rope_or_plan_block(int id, const __nv_bfloat16 *q, const int *seq_lens, int rows, int s_q,
+                                                   int H, float base, __nv_bfloat16 *__restrict__ q_abs,
+                                                   const PlanArgs &plan, int *scratch, int cap) {
+    const double theta = rope_theta(threadIdx.x % 32, 64, base);
+    step_wait_prev();
     if (id == 0) {
         plan_block<256>(plan, scratch, cap);
         return;
     }
     const int wpr = rope_warps(rows), u = (id - 1) * 8 + (int)threadIdx.x / 32, lane = threadIdx.x % 32;
     const int row = u / wpr, first = u % wpr;
-    if (row >= rows) {
-        step_wait_prev();
-        return;
-    }
+    if (row >= rows) return;
     constexpr int U = 16;
     const int b = row / s_q, j = row % s_q;
     const __nv_bfloat16 *src = q + (size_t)row * H * ROPE_D_QK + 128 + 2 * lane;
@@ -53,8 +51,7 @@ __device__ __forceinline__ void rope_or_plan_block(int id, const __nv_bfloat16 *
     };
     load(first);
     float cs, sn;
-    rope_cos_sin(query_pos(plan.view, seq_lens, b, j, s_q), lane, 64, base, &cs, &sn);
-    step_wait_prev();
+    rope_cos_sin(query_pos(plan.view, seq_lens, b, j, s_q), theta, &cs, &sn);
     for (int h0 = first; h0 < H; h0 += U * wpr) {
         uint32_t y[U];
 #pragma unroll
