@@ -221,9 +221,10 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
                     uint8_t *d = const_cast<uint8_t *>(q < 32 ? tkv + (q / 8) * BLK : tkr) + r * 128 + 16 * (q % 8);
                     *reinterpret_cast<uint4 *>(d) = make_uint4(0u, 0u, 0u, 0u);
                 }
+                tc::fence_proxy_async_smem();   // any page may be such a one, and its stage is refilled by a copy
                 __syncwarp();
             }
-        } else if (valid < 16 * warp + 16) {   // this warp's rows past the chunk's end: zero them
+        } else if (valid < 16 * warp + 16) {   // this warp's rows past the chunk's end: zero them (no refill follows)
             for (int e = lane; e < 16 * 5 * 8; e += 32) {
                 const int r = 16 * warp + e / 40, q = e % 40;   // 40 chunks of 16 B per row (4 KV blocks + k^R)
                 if (r < valid) continue;
