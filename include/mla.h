@@ -493,8 +493,9 @@ MLA_API mla_status mla_select_path(const mla_dims *dims, int32_t batch, int32_t 
  * mla_debug_decode_fault — test hook of the bounded device waits (failure detection).  The
  * pages have no counterpart to it.  After a call with withhold_step >= 0, every tensor-core
  * absorbed decode launched from the calling thread skips the completion signal of pipeline
- * step `withhold_step` (the PV product of that 128-token step) in every CTA pair, so the waits
- * on it run out: the kernel records MLA_ERR_TIMEOUT in the device error word, stops issuing
+ * step `withhold_step` (the PV product of that 128-token step) in every CTA pair, and the tensor-core
+ * products per head around a tree's or window's decode that of their block of that number (the absorption
+ * has one, the projection one per 64 latent columns), so the waits on it run out: the kernel records MLA_ERR_TIMEOUT in the device error word, stops issuing
  * work, frees its tensor memory and returns without faulting; the call's output is garbage and
  * mla_get_device_status() reports MLA_ERR_TIMEOUT.  wait_us (1..2000000) replaces the 2 s limit
  * of every device wait, so the test ends in milliseconds; 0 keeps the default.

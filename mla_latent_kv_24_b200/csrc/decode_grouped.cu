@@ -355,9 +355,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     }
     if (!ok) {   // a wait ran out: let copies in flight land before the memory is released
         if (lane == 0) report(p.err, MLA_ERR_TIMEOUT);
-        const uint64_t t0 = tc::globaltimer();
-        while (tc::globaltimer() - t0 < 200000ull) {
-        }
+        tc::drain_copies();
     }
     __syncthreads();   // the stage buffers become the reduction buffer
 

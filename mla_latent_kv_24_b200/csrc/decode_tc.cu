@@ -679,9 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (*c.abort_flag) {
         // A wait ran out: give any tile copies still in flight time to land before the
         // shared memory they target is released.
-        const uint64_t t0 = tc::globaltimer();
-        while (tc::globaltimer() - t0 < 200000ull) {
-        }
+        tc::drain_copies();
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -775,6 +773,7 @@ void tc_set_test_fault(int withhold_step, uint64_t wait_ns) {
     g_test_withhold = withhold_step < 0 ? -1 : withhold_step;
     g_test_wait_ns = wait_ns == 0 ? WAIT_NS : wait_ns;
 }
+WaitRule tc_wait_rule() { return WaitRule{g_test_wait_ns, g_test_withhold}; }
 
 bool tc_available() { return true; }
 int tc_units(int sms) { return sms / 2; }

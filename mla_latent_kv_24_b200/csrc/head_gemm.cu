@@ -10,8 +10,8 @@
 // and 256 KB of partials read per row, against 17 and 34 MFLOP.  For 512 rows of one chunk the absorption takes 35 us
 // (3.3 TB/s), the projection 49 (3.4 TB/s); for 128 rows of two chunks 14 and 21.
 //
-// Every wait is bounded; a wait that runs out records MLA_ERR_TIMEOUT, and the CTA still frees its tensor
-// memory.  The next kernel may launch only once a CTA holds its tensor memory: CTAs of two kernels share an
+// Every wait is bounded.  A wait that runs out records MLA_ERR_TIMEOUT and ends the CTA's work: nothing more is
+// issued or stored, copies in flight get time to land, and the tensor memory is freed.  The next kernel may launch only once a CTA holds its tensor memory: CTAs of two kernels share an
 // SM's 512 columns, and one that waits for its predecessor must not hold what the predecessor still needs.
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -28,7 +28,6 @@ namespace {
 constexpr int D_C = 512, D_N = 128, D_R = 64, D_QK = 192, D_OUT = 576, D_V = 128;
 constexpr int TM = 128;                        // rows of a tile
 constexpr uint32_t BLK = TM * 128;             // 128 rows x 64 bf16, 128-byte swizzled
-constexpr uint64_t WAIT_NS = 2000000000ull;
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
     asm volatile(
@@ -99,7 +98,8 @@ __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ 
                                                         const __grid_constant__ CUtensorMap tm_w,
                                                         const __nv_bfloat16 *q, const __nv_bfloat16 *W_uk,
                                                         const int *seq_lens, int rows, int s_q, int H, int hpw,
-                                                        float base, __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan) {
+                                                        float base, __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan,
+                                                        WaitRule wr) {
     extern __shared__ uint8_t hsm[];
     const int h = blockIdx.x, n0 = blockIdx.y * 256, row0 = blockIdx.z * TM;
     if (h >= H) {
@@ -115,24 +115,35 @@ __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ 
     step_wait_prev();   // queries may come from the kernel before, and q_abs is workspace that it may still read
     const uint32_t full = s.base + AB_BAR, done = full + 8;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    bool ok = true;
     if (threadIdx.x == 0) {
         tc::mbar_arrive_expect_tx(full, 6 * BLK);
         for (int i = 0; i < 2; ++i) tma_load_3d(s.base + AB_A + BLK * i, &tm_q, 64 * i, h, row0, full);
         for (int i = 0; i < 4; ++i) tma_load_2d(s.base + AB_B + BLK * i, &tm_w, n0 + 64 * i, (h / hpw) * D_N, full);
-        if (tc::mbar_wait_spin(full, 0, WAIT_NS)) {
+        ok = tc::mbar_wait_spin(full, 0, wr.limit_ns);
+        if (ok) {
             tc::fence_after_sync();
             const uint64_t a = tc::sdesc_sw128(s.base + AB_A, 16, 1024), b = tc::sdesc_sw128(s.base + AB_B, BLK, 1024);
 #pragma unroll
             for (int k = 0; k < D_N / 16; ++k)
                 mma(s.tmem, tc::sdesc_add(a, (k / 4) * BLK + 32 * (k % 4)), tc::sdesc_add(b, 2048 * k), AB_IDESC, k > 0);
-        } else {
-            report(plan.err, MLA_ERR_TIMEOUT);
+            if (wr.withhold != 0) commit(done);
         }
-        commit(done);
     }
     __syncwarp();
-    if (!tc::mbar_wait(done, 0, 2 * WAIT_NS)) report(plan.err, MLA_ERR_TIMEOUT);
-    __syncthreads();   // every thread has passed the wait: the operands are read
+    // The operand wait comes before this one: twice the limit for the threads that wait from the start.
+    if (ok) ok = tc::mbar_wait(done, 0, 2 * wr.limit_ns);
+    if (__syncthreads_or(!ok)) {   // else every thread has passed the wait: the operands are read
+        if (threadIdx.x == 0) report(plan.err, MLA_ERR_TIMEOUT);
+        tc::drain_copies();
+        tc::fence_before_sync();
+        __syncthreads();
+        if (warp == 0) {
+            tc::fence_after_sync();
+            tmem_free(s.tmem, 256);
+        }
+        return;
+    }
     tc::fence_after_sync();
     __nv_bfloat16 *stage = reinterpret_cast<__nv_bfloat16 *>(s.sbase);
     const int r = 32 * (warp % 4) + lane;          // TMEM lane = row; warps 4-7 take the second 128 columns
@@ -184,7 +195,8 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
                                                             const float *__restrict__ part_o,
                                                             const float *__restrict__ part_ml,
                                                             const int *__restrict__ row_first, int rows, int H, int hpw,
-                                                            __nv_bfloat16 *__restrict__ out, bool keep_empty, int *err) {
+                                                            __nv_bfloat16 *__restrict__ out, bool keep_empty, int *err,
+                                                            WaitRule wr) {
     extern __shared__ uint8_t hsm[];
     const Setup s = set_up<P_COUNT>(hsm, PJ_BAR, 128);
     step_allow_next();
@@ -247,11 +259,12 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
             v[i] = (held >> (NR * e + i)) & 1u ? __ldcs(src[i] + (KB * e + kb) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     bool ok = true;
-    // Block kb, whose first chunks are in v; refill() fetches what v is to hold next.
+    // Block kb, whose first chunks are in v; refill() fetches what v is to hold next.  A thread whose wait has run out
+    // waits no more, issues nothing more, and meets the others at the end.
     auto block = [&](int kb, float4 (&v)[NR], auto merge, auto refill) {
         const int st = kb & 1;
         uint8_t *hi = s.sbase + PJ_STAGE * st, *lo = hi + BLK;
-        if (kb >= 2 && !tc::mbar_wait(bar(P_EMPTY + st), ((kb >> 1) - 1) & 1, WAIT_NS)) ok = false;
+        if (kb >= 2 && ok) ok = tc::mbar_wait(bar(P_EMPTY + st), ((kb >> 1) - 1) & 1, wr.limit_ns);
 #pragma unroll
         for (int i = 0; i < NR; ++i) v[i].x *= w0[i], v[i].y *= w0[i], v[i].z *= w0[i], v[i].w *= w0[i];
         merge();
@@ -269,7 +282,8 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
         tc::fence_proxy_async_smem();
         __syncthreads();
         if (tid == 0) {
-            if (tc::mbar_wait_spin(bar(P_FULL + st), (kb >> 1) & 1, WAIT_NS)) {
+            if (ok) ok = tc::mbar_wait_spin(bar(P_FULL + st), (kb >> 1) & 1, wr.limit_ns);
+            if (ok) {
                 tc::fence_after_sync();
                 const uint64_t ah = tc::sdesc_sw128(s.base + PJ_STAGE * st, 16, 1024);
                 const uint64_t b = tc::sdesc_add(ah, 2 * BLK);
@@ -278,14 +292,12 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
                     mma(s.tmem, tc::sdesc_add(ah, 32 * k), tc::sdesc_add(b, 32 * k), PJ_IDESC, kb > 0 || k > 0);
                     mma(s.tmem, tc::sdesc_add(ah, BLK + 32 * k), tc::sdesc_add(b, 32 * k), PJ_IDESC, true);
                 }
-            } else {
-                ok = false;
+                if (kb != wr.withhold) commit(bar(P_EMPTY + st));
             }
-            commit(bar(P_EMPTY + st));
         } else if (tid == 128 && kb >= 1 && kb + 1 < KB) {
             // The W_UV block after this one takes the place of the one before it.
-            if (tc::mbar_wait(bar(P_EMPTY + (st ^ 1)), ((kb - 1) >> 1) & 1, WAIT_NS)) load_w(kb + 1);
-            else ok = false;
+            if (ok) ok = tc::mbar_wait(bar(P_EMPTY + (st ^ 1)), ((kb - 1) >> 1) & 1, wr.limit_ns);
+            if (ok) load_w(kb + 1);
         }
         __syncwarp();
     };
@@ -333,9 +345,18 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
             block(kb + 1, x1, [] {}, [&] { if (kb + 3 < KB) load(x1, 0, kb + 3); });
         }
     }
-    if (!tc::mbar_wait(bar(P_EMPTY + 1), ((KB - 1) >> 1) & 1, WAIT_NS)) ok = false;
-    if (!ok) report(err, MLA_ERR_TIMEOUT);
-    __syncwarp();
+    if (ok) ok = tc::mbar_wait(bar(P_EMPTY + 1), ((KB - 1) >> 1) & 1, wr.limit_ns);
+    if (__syncthreads_or(!ok)) {
+        if (tid == 0) report(err, MLA_ERR_TIMEOUT);
+        tc::drain_copies();
+        tc::fence_before_sync();
+        __syncthreads();
+        if (warp == 0) {
+            tc::fence_after_sync();
+            tmem_free(s.tmem, 128);
+        }
+        return;
+    }
     tc::fence_after_sync();
     const int row = row0 + 32 * (warp % 4) + lane, col = 32 * (warp / 4);
     float v[32];
@@ -401,7 +422,8 @@ cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, con
     cudaError_t e = raise_smem_limit((const void *)absorb_tc_kernel, AB_SMEM);
     if (e != cudaSuccess) return e;
     MLA_STEP_LAUNCH(absorb_tc_kernel, grid, dim3(256), AB_SMEM, st, tm_q, tm_w, (const __nv_bfloat16 *)q,
-                    (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs, plan);
+                    (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs, plan,
+                    tc_wait_rule());
     return cudaGetLastError();
 }
 
@@ -413,7 +435,7 @@ cudaError_t launch_project_tc(const Dims &d, const float *part_o, const float *p
     cudaError_t e = raise_smem_limit((const void *)project_tc_kernel, PJ_SMEM);
     if (e != cudaSuccess) return e;
     MLA_STEP_LAUNCH(project_tc_kernel, dim3(d.H, ceil_div(rows, TM)), dim3(PJ_THREADS), PJ_SMEM, st, tm_w, part_o, part_ml,
-                    row_first, rows, d.H, d.hpw, (__nv_bfloat16 *)out, keep_empty, err);
+                    row_first, rows, d.H, d.hpw, (__nv_bfloat16 *)out, keep_empty, err, tc_wait_rule());
     return cudaGetLastError();
 }
 

@@ -406,9 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (c.rank == 0 && lane == 0) run_pv_issuer(c, p, u, tmem);
     }
     if (*c.abort_flag) {   // a wait ran out: let copies in flight land before the memory is released
-        const uint64_t t0 = tc::globaltimer();
-        while (tc::globaltimer() - t0 < 200000ull) {
-        }
+        tc::drain_copies();
     }
     tc::fence_before_sync();
     __syncthreads();

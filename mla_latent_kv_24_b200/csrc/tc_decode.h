@@ -25,10 +25,15 @@ cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, con
 cudaError_t launch_project_tc(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
                               const void *W_uv, void *out, int *err, cudaStream_t st, bool keep_empty);
 
-// Test hook of the bounded waits: later tcgen05 decodes on the calling thread skip the completion
-// signal of pipeline step `withhold_step` (-1: none) and give up every wait after `wait_ns`
-// (0: the default 2 s).
+// Test hook of the bounded waits: later tcgen05 decodes on the calling thread, and the per-head products
+// around them, skip the completion signal of pipeline step `withhold_step` (-1: none) and give up every
+// wait after `wait_ns` (0: the default 2 s).
 void tc_set_test_fault(int withhold_step, uint64_t wait_ns);
+struct WaitRule {
+    uint64_t limit_ns;
+    int withhold;   // -1: none
+};
+WaitRule tc_wait_rule();   // of the calling thread
 
 // Grouped path, bf16, d_nope = d_v = 128, d_rope = 64, heads_per_group = 8.
 bool grouped_tc_ok(const Dims &d, int s_q);   // s_q <= 4: 16-row tiles of 8 heads x 2 queries

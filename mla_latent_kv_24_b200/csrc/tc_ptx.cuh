@@ -96,6 +96,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// After a wait that ran out: time for the copies and products still in flight to end before the shared
+// and tensor memory that they use is given back.
+__device__ __forceinline__ void drain_copies() {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 200000ull) {
+    }
+}
+
 // Bounded wait without the suspend hint, for the single threads that issue MMAs: they resume as
 // soon as the phase completes (a thread suspended with a hint resumes later), and one such thread
 // per role costs the softmax warps little.
