@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__res
                 *p.entry(d, full) = -1;
                 p.refs[to] = 0;
             }
-        } else if (rem && sets.n) {
+        } else if (rem) {   // reported with and without caches to copy in
             if (from >= p.n_pages || to < 0 || to >= p.n_pages) {
                 if (threadIdx.x == 0) report(p.err, MLA_ERR_DEVICE_BOUNDS);
             } else {
