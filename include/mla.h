@@ -276,10 +276,10 @@ MLA_API mla_status mla_cache_reserve(const mla_dims *dims, const int32_t *new_le
  * mla_cache_fork — requests dst_req[i] become copies of what requests src_req[i] were before the call
  * (device [n_fork] each): full pages are shared (page_refs counts the new holder), the rows of a partly
  * filled last page are copied into a new page, so that source and copy can both grow, and dropped entries
- * stay dropped.  Full pages are shared with the drafted nodes in them: fork a source while it has none
- * (before they are reserved, or after mla_cache_accept).  The destinations must be empty (seq_lens 0),
- * each named once; a source may be named
- * many times.  A bad index or length or a destination in use (MLA_ERR_DEVICE_BOUNDS) or too few free
+ * stay dropped (a dropped last page takes no page; while there are enough, the id of its turn is passed over).
+ * Full pages are shared with the drafted nodes in them: fork a source while it has none (before they
+ * are reserved, or after mla_cache_accept).  The destinations must be empty (seq_lens 0), each named once; a
+ * source may be named many times.  A bad index or length or a destination in use (MLA_ERR_DEVICE_BOUNDS) or too few free
  * pages (MLA_ERR_NO_PAGES) leaves everything as it was.  A page id outside the pool is reported
  * (MLA_ERR_DEVICE_BOUNDS), and its rows are not copied.
  */

@@ -176,10 +176,14 @@ __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restri
 // Checks and new pages.  Claims the destinations (which must be empty, each named once) by a compare
 // and swap of their length, so that a destination named twice is found whatever the order.  A call
 // that is carried out leaves -1 - length in every destination, which tells the copying blocks so.
+//
+// A fork takes a page for its source's partly filled last page.  Where the source has dropped that page, the
+// copying blocks give it back.  If the pool is short of pages for that, the sources' entries are read here, and
+// those forks take none: reading them always would put a load into the chain of every call (forks of one request 10.7 -> 11.9 us).
 __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
                                                        int n) {
     step_begin();
-    __shared__ int len[CAP];
+    __shared__ int len[CAP];   // the source's length; -1 - length where its partial last page is known to be dropped
     const uint32_t tile = first_bits(p);
     const int per = ceil_div(n, PT), i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
     int parts = 0, bad = 0;
@@ -203,18 +207,17 @@ __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__rest
                 break;
             }
     bad = __syncthreads_or(bad);
-    int total;
-    int rank0 = block_prefix(parts, &total);
     // No destination has pages of its own, so its row holds nothing that is still needed.
-    bool ok = !bad;
-    if (ok) {
-        // The rank-th partial page goes to the rank-th fork with one: each thread's forks are
-        // consecutive, so a rank names a thread's first rank and a count from there.
-        __shared__ int first_rank[PT + 1];
+    // The rank-th page goes to the rank-th fork with a partial page (a dropped one has a negative length): each
+    // thread's forks are consecutive, so a rank names a thread's first rank and a count from there.
+    __shared__ int first_rank[PT + 1];
+    auto hand_out = [&](int mine) {
+        int total;
+        const int rank0 = block_prefix(mine, &total);
         first_rank[threadIdx.x] = rank0;
         if (threadIdx.x == PT - 1) first_rank[PT] = total;
         __syncthreads();
-        ok = allocate(p.refs, p.n_pages, total, tile, [&](int rank, int pg) {
+        return allocate(p.refs, p.n_pages, total, tile, [&](int rank, int pg) {
             int lo = 0, hi = PT - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
@@ -226,6 +229,26 @@ __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__rest
                 if (len[i] % p.page > 0 && skip-- == 0) break;
             *p.entry(dst[i], len[i] / p.page) = pg;
         });
+    };
+    bool ok = !bad;
+    if (ok) {
+        ok = hand_out(parts);
+        if (!ok) {
+            int none = 0;   // forks that need no page after all
+            for (int i = i0; i < i1; ++i) {
+                const int L = len[i];
+                if (L % p.page == 0 || *p.entry(src[i], L / p.page) >= 0) continue;
+                len[i] = -1 - L;
+                ++none;
+            }
+            if (__syncthreads_or(none)) ok = hand_out(parts - none);
+            __syncthreads();   // the searches have read the lengths
+            for (int i = i0; i < i1; ++i)
+                if (len[i] < 0) {
+                    len[i] = -1 - len[i];
+                    if (ok) *p.entry(dst[i], len[i] / p.page) = -1;
+                }
+        }
     }
     __syncthreads();
     for (int i = i0; i < i0 + n_claimed; ++i) p.seq_lens[dst[i]] = ok ? -1 - len[i] : 0;
@@ -271,7 +294,7 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__res
             else if (pg >= 0) atomicAdd(p.refs + pg, 1);          // a dropped page (< 0) has no holder to add
         }
         const int from = rem ? *p.entry(s, full) : -1, to = rem ? *p.entry(d, full) : -1;
-        if (rem && from < 0) {   // dropped in the source: so it is in the copy, and the page meant for it is free again
+        if (rem && from < 0) {   // dropped in the source: so it is in the copy, and a page taken for it is free again
             cooperative_groups::this_cluster().sync();   // every block has read the entries
             if (rank == 0 && threadIdx.x == 0 && to >= 0 && to < p.n_pages) {
                 *p.entry(d, full) = -1;

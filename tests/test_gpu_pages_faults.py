@@ -29,3 +29,78 @@ def test_a_partial_page_outside_the_pool_is_reported_without_caches_too(cached, 
     p.lens[1] = 100
     p.check()
     assert p.refs[keep] == 1
+
+
+def dropped_pool(free_pages):
+    """Request 0 has dropped its partly filled last page, request 1 has not; `free_pages` pages are free."""
+    p = Pool("dsv2", (100, 70, 0, 0, 0, 0), 3 + max(1, free_pages), layers=2, seed=free_pages)
+    p.both("release", (0,), (1,), (2,))
+    p.refs[p.free()[free_pages:]] = 1                       # someone else's
+    p.upload()
+    assert len(p.free()) == free_pages
+    return p
+
+
+def m_fork_dropped(p, src, dst, ids):
+    for s, d in zip(src, dst):
+        full, rem = divmod(int(p.lens[s]), p.page)
+        p.table[d, :full] = p.table[s, :full]
+        p.refs[p.table[s, :full]] += 1
+        if rem and p.table[s, full] < 0:
+            p.table[d, full] = -1
+        elif rem:
+            p.table[d, full] = pg = ids.pop(0)
+            p.refs[pg] = 1
+            p.lat[:, pg, :rem] = p.lat[:, p.table[s, full], :rem]
+        p.lens[d] = p.lens[s]
+
+
+def test_a_fork_that_needs_no_page_is_carried_out_in_a_full_pool():
+    p = dropped_pool(0)
+    fork(p, (0, 0), (2, 4))
+    mla.mla_get_device_status()
+    m_fork_dropped(p, (0, 0), (2, 4), [])
+    p.check()
+    fork(p, (0, 1), (3, 5))                                 # the second needs one
+    refused(7)
+    p.check()
+
+
+@pytest.mark.parametrize("n_free", [1, 2])
+def test_dropped_pages_have_no_turn_where_pages_are_few(n_free):
+    p = dropped_pool(n_free)
+    free = p.free()
+    fork(p, (0, 1, 0), (2, 3, 4))
+    mla.mla_get_device_status()
+    m_fork_dropped(p, (0, 1, 0), (2, 3, 4), free[:1])
+    p.check()
+
+
+def test_dropped_pages_pass_their_turn_over():
+    p = dropped_pool(5)
+    free = p.free()
+    src, dst = (0, 1, 0, 1), (2, 3, 4, 5)
+    fork(p, src, dst)
+    mla.mla_get_device_status()
+    m_fork_dropped(p, src, dst, [free[1], free[3]])
+    p.check()
+
+
+def test_many_forks_of_sources_with_and_without_their_last_page():
+    # more forks than the planning block has threads, and pages in several tiles of its scan
+    n = 1500
+    p = Pool("fp32", (20, 5) + (0,) * n, 3000, seed=8)
+    p.both("release", (0,), (1,), (2,))
+    src = [i % 3 % 2 for i in range(n)]
+    dst = list(range(2, 2 + n))
+    for few in (False, True):
+        if few:
+            p.both("release", tuple(dst))
+            free = p.free()
+            p.refs[free[sum(src) + 10:]] = 1
+            p.upload()
+        free = p.free()
+        fork(p, src, dst)
+        mla.mla_get_device_status()
+        m_fork_dropped(p, src, dst, free[:] if few else [free[i] for i in range(n) if src[i]])
+        p.check()
