@@ -12,6 +12,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.h"
 
@@ -175,14 +176,22 @@ __global__ void __launch_bounds__(PT) reserve_kernel(Pool p, const int *__restri
 // ------------------------------------------------------------------------------------- fork
 // Checks and new pages.  Claims the destinations (which must be empty, each named once) by a compare
 // and swap of their length, so that a destination named twice is found whatever the order.  A call
-// that is carried out leaves -1 - length in every destination, which tells the copying blocks so.
+// that is carried out leaves -1 - length in every destination, which tells the copying blocks the length.
+// A destination of a refused call keeps its own, which may be anything, such a mark too; so a refused call also
+// leaves its number in a word of its own.  (Numbers FORK_WORDS apart share a word, which names one of them;
+// a captured call keeps its number, and clears what an earlier replay left.)
 //
 // A fork takes a page for its source's partly filled last page.  Where the source has dropped that page, the
 // copying blocks give it back.  If the pool is short of pages for that, the sources' entries are read here, and
 // those forks take none: reading them always would put a load into the chain of every call (forks of one request 10.7 -> 11.9 us).
+constexpr int FORK_WORDS = 4096;
+__device__ unsigned long long g_fork_refused[FORK_WORDS];
+
 __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
-                                                       int n) {
+                                                       int n, unsigned long long call) {
     step_begin();
+    unsigned long long left = 0;
+    if (threadIdx.x == 0) left = g_fork_refused[call % FORK_WORDS];
     __shared__ int len[CAP];   // the source's length; -1 - length where its partial last page is known to be dropped
     const uint32_t tile = first_bits(p);
     const int per = ceil_div(n, PT), i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
@@ -252,7 +261,10 @@ __global__ void __launch_bounds__(PT) fork_plan_kernel(Pool p, const int *__rest
     }
     __syncthreads();
     for (int i = i0; i < i0 + n_claimed; ++i) p.seq_lens[dst[i]] = ok ? -1 - len[i] : 0;
-    if (!ok && threadIdx.x == 0) report(p.err, bad ? MLA_ERR_DEVICE_BOUNDS : MLA_ERR_NO_PAGES);
+    if (threadIdx.x == 0) {
+        if (!ok) report(p.err, bad ? MLA_ERR_DEVICE_BOUNDS : MLA_ERR_NO_PAGES);
+        if (!ok || left == call) g_fork_refused[call % FORK_WORDS] = ok ? 0 : call;
+    }
 }
 
 // Copies bytes [from, to) of a span with the block's threads.
@@ -276,15 +288,14 @@ __device__ __forceinline__ void copy_span(char *dst, const char *src, size_t byt
 // destination its length.  A piece of rows goes to one block, or in parts to several when there are
 // fewer pieces than blocks.
 __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__restrict__ src, const int *__restrict__ dst,
-                                                        RowSets sets) {
+                                                        RowSets sets, unsigned long long call) {
     step_begin();
     const int rank = blockIdx.x, blocks = gridDim.x;              // the cluster spans the grid's x
+    const unsigned long long refused = g_fork_refused[call % FORK_WORDS];
     const int s = src[blockIdx.y], d = dst[blockIdx.y];
-    int L = -1;   // < 0: refused as a whole
-    if (s >= 0 && s < p.batch && d >= 0 && d < p.batch) {
-        L = -1 - p.seq_lens[d];
-        if (L > 0 && L != p.seq_lens[s]) L = -1;   // no marker: a length that cannot be, which refused the call
-    }
+    if (refused == call || s < 0 || s >= p.batch || d < 0 || d >= p.batch) return;   // the whole cluster
+    const int L = -1 - p.seq_lens[d];
+    if (L < 0 || (L > 0 && L != p.seq_lens[s])) return;   // not a mark of this call: nothing to index by
     if (L > 0) {
         const int full = L / p.page, rem = L % p.page;
         for (int k = rank * (int)blockDim.x + (int)threadIdx.x; k < full; k += blocks * (int)blockDim.x) {
@@ -325,8 +336,8 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(Pool p, const int *__res
             }
         }
     }
-    cooperative_groups::this_cluster().sync();   // every block has read the length's marker
-    if (rank == 0 && threadIdx.x == 0 && L >= 0) p.seq_lens[d] = L;
+    cooperative_groups::this_cluster().sync();   // every block has read the mark
+    if (rank == 0 && threadIdx.x == 0) p.seq_lens[d] = L;
 }
 
 // ------------------------------------------------------------------------------------- release
@@ -503,9 +514,11 @@ cudaError_t launch_cache_reserve(const PagePool &a, const int *new_lens, cudaStr
 
 cudaError_t launch_cache_fork(const PagePool &a, const int *src, const int *dst, int n_fork, const PageRows *rows, int n_rows,
                               cudaStream_t st) {
+    static std::atomic<unsigned long long> calls{0};
     const Pool p = pool_of(a);
-    MLA_STEP_LAUNCH(fork_plan_kernel, dim3(1), dim3(PT), 0, st, p, src, dst, n_fork);
-    return launch_clusters(fork_copy_kernel, 8, 256, n_fork, st, p, src, dst, sets_of(rows, n_rows));
+    const unsigned long long call = calls.fetch_add(1, std::memory_order_relaxed) + 1;   // never 0
+    MLA_STEP_LAUNCH(fork_plan_kernel, dim3(1), dim3(PT), 0, st, p, src, dst, n_fork, call);
+    return launch_clusters(fork_copy_kernel, 8, 256, n_fork, st, p, src, dst, sets_of(rows, n_rows), call);
 }
 
 cudaError_t launch_cache_release(const PagePool &a, const int *req, const int *first, const int *last, int n_req,

@@ -104,3 +104,49 @@ def test_many_forks_of_sources_with_and_without_their_last_page():
         mla.mla_get_device_status()
         m_fork_dropped(p, src, dst, free[:] if few else [free[i] for i in range(n) if src[i]])
         p.check()
+
+
+@pytest.mark.parametrize("src,dst,length", [
+    ((0,), (2,), -101),                 # the mark that a carried-out fork of request 0 (100 tokens) would leave
+    ((0, 1, 0), (2, 3, 4), -101),
+    ((1, 0), (3, 2), -101),
+    ((1,), (2,), -65),
+    ((4,), (2,), -1),                   # of an empty source
+    ((0,), (2,), -1),
+    ((0, 4), (3, 2), -1),
+    ((0,), (2,), -2 ** 31),
+])
+def test_a_refused_fork_leaves_any_length(src, dst, length):
+    p = Pool("dsv2", (100, 64, 0, 0, 0), 12, layers=2, seed=3)
+    p.lens[2] = length
+    p.upload()
+    for cached in (True, False):
+        fork(p, src, dst, cached)
+        refused(5)
+        p.check()
+
+
+def test_a_captured_fork_refused_in_one_replay_and_not_in_the_next():
+    import torch
+    p = Pool("dsv2", (100, 64, 0, 0), 12, layers=2, seed=4)
+    src, dst, tail = p.i32((0,)), p.i32((2,)), p.tail()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mla.mla_cache_fork(p.dims, src, dst, 1, *tail, p.d_lat, None, p.layers)
+    for rounds in range(3):
+        for length in (-101, 64, -1):
+            p.lens[2] = length
+            p.d_lens.copy_(torch.from_numpy(p.lens))
+            g.replay()
+            refused(5)
+            p.check()
+        p.lens[2] = 0
+        p.d_lens.copy_(torch.from_numpy(p.lens))
+        for _ in range(2):
+            g.replay()
+            mla.mla_get_device_status()
+            p.m_fork((0,), (2,))
+            p.check()
+            p.both("release", (2,))
+    del g
