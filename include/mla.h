@@ -38,6 +38,7 @@
  *     tokens t <= that position (this gives the causal mask between MTP query tokens).
  *     Token t of request b lives in page page_table[b*max_pages + t/page_size], row
  *     t % page_size.
+ *     A decode call takes up to 2^20 query rows (batch x s_q, for a tree batch x max_nodes).
  *   - Errors: every call returns mla_status.  MLA_ERR_CUDA carries detail in
  *     mla_last_error_string().  Conditions only the device can see (a page id or slot out of
  *     range, device seq_lens that contradict the host copy, a pipeline wait that ran out)

@@ -27,19 +27,20 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *q, const T *W_uk
                                                        int H, int hpw, int d_c, int d_r, int d_n, float base,
                                                        T *__restrict__ q_abs, PlanArgs plan) {
     step_allow_next();
-    if (blockIdx.x < H && blockIdx.y == 0 && (int)threadIdx.x < d_n)   // d_c is a multiple of 8
+    if (blockIdx.x < H && grid_tile() == 0 && (int)threadIdx.x < d_n)   // d_c is a multiple of 8
         prefetch_l2(W_uk + ((size_t)(blockIdx.x / hpw) * d_n + threadIdx.x) * d_c, d_c * (uint32_t)sizeof(T));
     const double theta = rope_theta(threadIdx.x % (d_r / 2), d_r, base);   // of this thread's first pair
     step_wait_prev();
     __shared__ float qn[RB][128];
     if (blockIdx.x == H) {
         static_assert(sizeof(qn) >= sizeof(int) * (2 * 512 + 1), "the plan's scratch");
-        if (blockIdx.y == 0) plan_block<256>(plan, reinterpret_cast<int *>(qn), 512);
+        if (grid_tile() == 0) plan_block<256>(plan, reinterpret_cast<int *>(qn), 512);
         return;
     }
     const int h = blockIdx.x, w = h / hpw;
-    const int row0 = blockIdx.y * RB;
+    const int row0 = grid_tile() * RB;
     const int nr = min(RB, rows - row0);
+    if (nr <= 0) return;
     const int d_qk = d_n + d_r, d_out = d_c + d_r;
     for (int i = threadIdx.x; i < RB * d_n; i += blockDim.x) {
         int r = i / d_n, k = i % d_n;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *q, const int *seq_
 cudaError_t launch_q_absorb(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch,
                             int s_q, void *q_abs, const PlanArgs &plan, cudaStream_t st) {
     const int rows = batch * s_q;
-    dim3 grid(d.H + 1, ceil_div(rows, RB));
+    const dim3 grid = tile_grid(d.H + 1, ceil_div(rows, RB));
     if (d.bf16)
         MLA_STEP_LAUNCH(q_absorb_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, (const __nv_bfloat16 *)q,
                         (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.d_c, d.d_r, d.d_n, d.base,

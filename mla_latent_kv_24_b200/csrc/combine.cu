@@ -28,8 +28,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
     step_begin();
     extern __shared__ float O[];  // [RB][DV]
     const int h = blockIdx.x;
-    const int row0 = blockIdx.y * RB;
+    const int row0 = grid_tile() * RB;
     const int nr = min(RB, rows - row0);
+    if (nr <= 0) return;
     for (int r = 0; r < nr; ++r) {
         const int pr = (row0 + r) / qpi, j = (row0 + r) % qpi;
         const int k0 = row_first[pr], k1 = row_first[pr + 1];
@@ -86,7 +87,8 @@ __global__ void __launch_bounds__(32 * RB) combine_view_kernel(const float *__re
     step_begin();
     extern __shared__ float O[];   // [RB][DV]
     __shared__ int kept[RB];
-    const int h = blockIdx.x, row0 = blockIdx.y * RB, nr = min(RB, rows - row0);
+    const int h = blockIdx.x, row0 = grid_tile() * RB, nr = min(RB, rows - row0);
+    if (nr <= 0) return;
     const int r = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (r < nr) {
         const int k0 = row_first[row0 + r], k1 = row_first[row0 + r + 1];
@@ -215,7 +217,7 @@ cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part
                             rows, qpi, d.H, DV, (float *)out);
         return cudaGetLastError();
     }
-    dim3 grid(d.H, ceil_div(rows, RB));
+    const dim3 grid = tile_grid(d.H, ceil_div(rows, RB));
     const size_t smem = sizeof(float) * RB * DV;
     if (d.bf16) {
         auto k = combine_kernel<__nv_bfloat16>;
@@ -235,8 +237,7 @@ cudaError_t launch_combine(const Dims &d, const float *part_o, const float *part
 
 cudaError_t launch_combine_view(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
                                 int DV, const void *W_uv, void *out, cudaStream_t st, bool keep_empty) {
-    if (ceil_div(rows, RB) > 65535) return cudaErrorInvalidValue;
-    const dim3 grid(d.H, ceil_div(rows, RB));
+    const dim3 grid = tile_grid(d.H, ceil_div(rows, RB));
     const size_t smem = sizeof(float) * RB * DV;   // at most 16 KiB
     if (d.bf16)
         MLA_STEP_LAUNCH(combine_view_kernel<__nv_bfloat16>, grid, dim3(32 * RB), smem, st, part_o, part_ml, row_first, rows,
@@ -289,7 +290,10 @@ __global__ void __cluster_dims__(XS, 1, 1) __launch_bounds__(256, 4)
     __nv_bfloat16 *Os = Ws + CN * X_LD;                               // [32 rows][128 c + 8]
     float *Red = reinterpret_cast<float *>(xsm);                     // [32][128], over Ws after the MMA
     const int s = (int)cluster.block_rank(), c0 = s * XC;
-    const int h = blockIdx.y, row0 = blockIdx.z * CM, nr = min(CM, rows - row0);
+    int h = blockIdx.y, tile = blockIdx.z;
+    if ((int)gridDim.y > H) tile = tile * ((int)gridDim.y / H) + h / H, h %= H;   // the heads several times over
+    const int row0 = tile * CM, nr = min(CM, rows - row0);
+    if (nr <= 0) return;   // the whole cluster
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const __nv_bfloat16 *W = W_uv + (size_t)(h / hpw) * CN * CK;
     // The W_UV slice streams in while the decode finishes: the decode has waited for all before the call.
@@ -484,8 +488,9 @@ cudaError_t launch_combine_mma(const Dims &d, const float *part_o, const float *
     const size_t smem = sizeof(__nv_bfloat16) * (size_t)(CN + CM_ROWS) * X_LD;
     static_assert(sizeof(float) * CM_ROWS * CN <= sizeof(__nv_bfloat16) * CN * X_LD, "Red fits over Ws");
     const int cm = fine ? CM_FINE : CM_ROWS;
-    if (ceil_div(rows, cm) > 65535 || d.H > 65535) return cudaErrorInvalidValue;
-    dim3 grid(XS, d.H, ceil_div(rows, cm));
+    // Grid: the cluster, heads (several times over where the row tiles pass a grid's 65,535), row tiles.
+    const int tiles = ceil_div(rows, cm), times = ceil_div(tiles, 65535);
+    dim3 grid(XS, d.H * times, ceil_div(tiles, times));
     auto k = layout == PART_OCTETS
                         ? (fine ? combine_split_kernel<true, true, CM_FINE> : combine_split_kernel<true, false, CM_ROWS>)
                         : (fine ? combine_split_kernel<false, true, CM_FINE> : combine_split_kernel<false, false, CM_ROWS>);

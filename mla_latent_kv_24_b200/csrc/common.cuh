@@ -51,6 +51,14 @@ __device__ __forceinline__ void rope_cos_sin(int pos, double theta, float *c, fl
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Row tiles over a grid's y and z, which hold 65,535 each: 2^20 rows in tiles of eight are twice that.  A few
+// blocks past the last tile may come with it.
+inline dim3 tile_grid(unsigned x, int tiles) {
+    const int z = ceil_div(tiles, 65535);
+    return dim3(x, ceil_div(tiles, z), z);
+}
+__device__ __forceinline__ int grid_tile() { return (int)(blockIdx.z * gridDim.y + blockIdx.y); }
+
 // ---------------------------------------------------------------------------------------
 // Programmatic dependent launch.  The kernels of a call are launched with programmatic stream
 // serialisation, so a kernel's CTAs may be launched while the previous kernel of the stream is
