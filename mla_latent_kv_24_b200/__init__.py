@@ -272,14 +272,15 @@ def mla_debug_decode_fault(withhold_step: int, wait_us: int = 0) -> None:
 # would be read past its end.
 # ---------------------------------------------------------------------------------------
 _torch = None   # the module, kept: an import statement costs 0.1 us of a call
+_INT = None     # torch.int32, the type of every index array, once torch is there
 
 
 def _here() -> int:
     """The current device; one that no tensor is on while CUDA has not been used."""
-    global _torch
+    global _torch, _INT
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _INT = torch, torch.int32
     return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -2
 
 
@@ -292,18 +293,23 @@ def _stream_on(stream, here) -> Optional[int]:
     return _stream(stream)
 
 
-def _arr(name, t, itemsize, n, here, optional=False) -> Optional[int]:
-    """Device address of a contiguous tensor of at least n elements of `itemsize` bytes on device `here`."""
+def _elt(dims):
+    """The type of a call's float tensors."""
+    return _torch.float32 if dims.dtype == MLA_FP32 else _torch.bfloat16
+
+
+def _arr(name, t, dtype, n, here, optional=False) -> Optional[int]:
+    """Device address of a contiguous tensor of at least n elements of `dtype` on device `here`."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is None")
-    if t.get_device() != here or t.itemsize != itemsize or t.numel() < n or not t.is_contiguous():
+    if t.get_device() != here or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         _dev(t)
         if t.get_device() != here:
             raise ValueError(f"{name} is on {t.device}, not on the current device")
-        if t.itemsize != itemsize:
-            raise ValueError(f"{name} has {t.itemsize}-byte elements, expected {itemsize}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} holds {t.dtype}, expected {dtype}")
         raise ValueError(f"{name} has {t.numel()} elements, expected at least {n}")
     return t.data_ptr()
 
@@ -321,11 +327,11 @@ def _host_lens(name, x, n):
 
 
 def _decode_view_args(dims, q, s_q, cache, n_pages_total, batch, max_pages, page_table, seq_lens, out, here):
-    e = 4 if dims.dtype == MLA_FP32 else 2
+    e = _elt(dims)
     rows = batch * s_q * dims.n_heads
     return e, (_arr("q", q, e, rows * (dims.d_nope + dims.d_rope), here),
                _arr("latent_cache", cache, e, n_pages_total * dims.page_size * (dims.d_c + dims.d_rope), here),
-               _arr("page_table", page_table, 4, batch * max_pages, here), _arr("seq_lens", seq_lens, 4, batch, here),
+               _arr("page_table", page_table, _INT, batch * max_pages, here), _arr("seq_lens", seq_lens, _INT, batch, here),
                _arr("out", out, e, rows * dims.d_v, here))
 
 
@@ -336,7 +342,7 @@ def _weights(dims, e, W_uk, W_uv, here):
 
 def _workspace(ws, nbytes, here):
     have = ws.numel() * ws.itemsize
-    return _arr("workspace", ws, ws.itemsize, 0, here), have if nbytes is None else min(nbytes, have)
+    return _arr("workspace", ws, ws.dtype, 0, here), have if nbytes is None else min(nbytes, have)
 
 
 def mla_decode_tree_workspace_size(dims, batch, max_nodes, seq_lens_host, n_nodes_host) -> int:
@@ -359,10 +365,11 @@ def mla_decode_tree(dims, q, W_uk, W_uv, latent_cache, page_table, seq_lens, n_n
                                                 page_table, seq_lens, out, here)
     uk, uv = _weights(dims, e, W_uk, W_uv, here)
     ws, nbytes = _workspace(workspace, workspace_bytes, here)
+    mask_type = _torch.uint64 if tree_mask is not None and tree_mask.dtype is _torch.uint64 else _torch.int64
     _check(load().mla_decode_tree(ctypes.byref(dims), qp, uk, uv, cp, tp, sp,
-                                  _arr("n_nodes", n_nodes, 4, batch, here), lp, np_,
-                                  _arr("depths", depths, 4, batch * max_nodes, here),
-                                  _arr("tree_mask", tree_mask, 8, batch * max_nodes, here), batch, max_nodes, max_pages,
+                                  _arr("n_nodes", n_nodes, _INT, batch, here), lp, np_,
+                                  _arr("depths", depths, _INT, batch * max_nodes, here),
+                                  _arr("tree_mask", tree_mask, mask_type, batch * max_nodes, here), batch, max_nodes, max_pages,
                                   n_pages_total, op, ws, nbytes, _stream_on(stream, here)))
 
 
@@ -409,24 +416,24 @@ def gqla_decode_window(dims, q, expanded_cache, latent_cache, page_table, seq_le
 
 def mla_cache_append_slots(dims, h, hidden, W_dkv, W_kr, req_idx, slots, positions, n_tok, page_table, batch,
                            max_pages, n_pages_total, latent_cache, stream=None) -> None:
-    e = 4 if dims.dtype == MLA_FP32 else 2
     row, here = dims.d_c + dims.d_rope, _here()
+    e = _elt(dims)
     _check(load().mla_cache_append_slots(
         ctypes.byref(dims), _arr("h", h, e, n_tok * hidden, here), hidden,
         _arr("W_dkv", W_dkv, e, dims.d_c * hidden, here, True),
-        _arr("W_kr", W_kr, e, dims.d_rope * hidden, here, True), _arr("req_idx", req_idx, 4, n_tok, here),
-        _arr("slots", slots, 4, n_tok, here), _arr("positions", positions, 4, n_tok, here), n_tok,
-        _arr("page_table", page_table, 4, batch * max_pages, here), batch, max_pages, n_pages_total,
+        _arr("W_kr", W_kr, e, dims.d_rope * hidden, here, True), _arr("req_idx", req_idx, _INT, n_tok, here),
+        _arr("slots", slots, _INT, n_tok, here), _arr("positions", positions, _INT, n_tok, here), n_tok,
+        _arr("page_table", page_table, _INT, batch * max_pages, here), batch, max_pages, n_pages_total,
         _arr("latent_cache", latent_cache, e, n_pages_total * dims.page_size * row, here), _stream_on(stream, here)))
 
 
 def _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here, refs_optional=False):
-    return (_arr("seq_lens", seq_lens, 4, batch, here), _arr("page_table", page_table, 4, batch * max_pages, here),
-            _arr("page_refs", page_refs, 4, n_pages_total, here, refs_optional))
+    return (_arr("seq_lens", seq_lens, _INT, batch, here), _arr("page_table", page_table, _INT, batch * max_pages, here),
+            _arr("page_refs", page_refs, _INT, n_pages_total, here, refs_optional))
 
 
 def _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total, here):
-    e = 4 if dims.dtype == MLA_FP32 else 2
+    e = _elt(dims)
     rows = n_layers * n_pages_total * dims.page_size
     g = dims.n_heads // max(1, dims.heads_per_group)
     return (_arr("latent_cache", latent_cache, e, rows * (dims.d_c + dims.d_rope), here, True),
@@ -437,7 +444,7 @@ def mla_cache_reserve(dims, new_lens, seq_lens, page_table, batch, max_pages, pa
                       stream=None) -> None:
     here = _here()
     s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here)
-    _check(load().mla_cache_reserve(ctypes.byref(dims), _arr("new_lens", new_lens, 4, batch, here), s, t, batch,
+    _check(load().mla_cache_reserve(ctypes.byref(dims), _arr("new_lens", new_lens, _INT, batch, here), s, t, batch,
                                     max_pages, r, n_pages_total, _stream_on(stream, here)))
 
 
@@ -446,8 +453,8 @@ def mla_cache_fork(dims, src_req, dst_req, n_fork, seq_lens, page_table, batch, 
     here = _here()
     s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here)
     lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total, here)
-    _check(load().mla_cache_fork(ctypes.byref(dims), _arr("src_req", src_req, 4, n_fork, here),
-                                 _arr("dst_req", dst_req, 4, n_fork, here), n_fork, s, t, batch, max_pages, r,
+    _check(load().mla_cache_fork(ctypes.byref(dims), _arr("src_req", src_req, _INT, n_fork, here),
+                                 _arr("dst_req", dst_req, _INT, n_fork, here), n_fork, s, t, batch, max_pages, r,
                                  n_pages_total, lat, exp, n_layers, _stream_on(stream, here)))
 
 
@@ -455,9 +462,9 @@ def mla_cache_release(dims, req_idx, first_page, last_page, n_req, seq_lens, pag
                       n_pages_total, stream=None) -> None:
     here = _here()
     s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here)
-    _check(load().mla_cache_release(ctypes.byref(dims), _arr("req_idx", req_idx, 4, n_req, here),
-                                    _arr("first_page", first_page, 4, n_req, here, True),
-                                    _arr("last_page", last_page, 4, n_req, here, True), n_req, s, t, batch, max_pages,
+    _check(load().mla_cache_release(ctypes.byref(dims), _arr("req_idx", req_idx, _INT, n_req, here),
+                                    _arr("first_page", first_page, _INT, n_req, here, True),
+                                    _arr("last_page", last_page, _INT, n_req, here, True), n_req, s, t, batch, max_pages,
                                     r, n_pages_total, _stream_on(stream, here)))
 
 
@@ -466,8 +473,8 @@ def mla_cache_accept(dims, ctx_lens, n_nodes, accepted, n_accepted, max_nodes, s
     here = _here()
     s, t, r = _pool_args(seq_lens, page_table, batch, max_pages, page_refs, n_pages_total, here, True)
     lat, exp = _cache_args(dims, latent_cache, expanded_cache, n_layers, n_pages_total, here)
-    _check(load().mla_cache_accept(ctypes.byref(dims), _arr("ctx_lens", ctx_lens, 4, batch, here),
-                                   _arr("n_nodes", n_nodes, 4, batch, here),
-                                   _arr("accepted", accepted, 4, batch * max_nodes, here),
-                                   _arr("n_accepted", n_accepted, 4, batch, here), max_nodes, s, t, batch, max_pages, r,
+    _check(load().mla_cache_accept(ctypes.byref(dims), _arr("ctx_lens", ctx_lens, _INT, batch, here),
+                                   _arr("n_nodes", n_nodes, _INT, batch, here),
+                                   _arr("accepted", accepted, _INT, batch * max_nodes, here),
+                                   _arr("n_accepted", n_accepted, _INT, batch, here), max_nodes, s, t, batch, max_pages, r,
                                    n_pages_total, lat, exp, n_layers, _stream_on(stream, here)))
