@@ -428,7 +428,11 @@ __device__ __forceinline__ void move_rows(const PageRows &rows, const Moves &m, 
 }
 
 // One cluster per request: moves the rows of every layer, then trims the request.
-constexpr int ACCEPT_THREADS = 288;   // 8 x 288 columns: the latent rows of 32 layers in one pass
+// 288 is the largest block of which an SM's registers hold four with the eight loads a thread has in flight
+// (56 each).  64 requests, latent rows of 8 / 27 / 60 / 128 layers, accept and a reserve: 192 threads 6.8 / 9.8 /
+// 11.9 / 18.1 us, 256: 7.0 / 8.2 / 13.1 / 18.5, 288: 6.8 / 8.6 / 11.5 / 17.0, 320: 6.6 / 8.8 / 12.1 / 18.4; one pass of
+// up to 1,024 threads instead of several: 6.6 / 8.2 / 14.0 / 19.5.
+constexpr int ACCEPT_THREADS = 288;
 
 __global__ void __launch_bounds__(ACCEPT_THREADS, 4) accept_kernel(Pool p, const int *__restrict__ ctx_lens,
                                                      const int *__restrict__ n_nodes, const int *__restrict__ accepted,
