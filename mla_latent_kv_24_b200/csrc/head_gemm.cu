@@ -401,15 +401,6 @@ bool encode_box(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, u
 
 }  // namespace
 
-// Above 16 rows, where the mma.sync form leaves its single wave (24 rows: 1.7 us a call less; 96: 4; the
-// kernel alone at 512 rows: 35 and 48).
-bool absorb_tc_pays(int rows) { return rows > 16; }
-// One 16-row tile merges faster in clusters of four CTAs a head (launch_combine_mma; a window's call of 8 rows 29 us
-// against 43, of 16 rows 34 and 37).  Above that a cluster takes its rows one pass after another, and this kernel a
-// row's chunks: rows^2 / 6 chunks in all are where the two meet (17 rows of 4.4 chunks 55 us in clusters, 65 here; 20
-// of 3.7: 57 and 62; 24 of 3.1: 65 and 64; 24 of one: 43 and 35; 32: 74 and 64; 40: 91 and 78).
-bool project_tc_pays(int rows, long long n_work) { return rows > 16 && 6 * n_work <= (long long)rows * rows; }
-
 cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch, int s_q,
                              void *q_abs, const PlanArgs &plan, cudaStream_t st) {
     const int rows = batch * s_q, z = ceil_div(rows, TM);

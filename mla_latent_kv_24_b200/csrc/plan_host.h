@@ -117,6 +117,17 @@ inline int plan_chunk_balanced(int batch, const Rows &rows, const Len &len_of, i
     return best;
 }
 
+// The kernels around a view's tcgen05 decode (head_gemm.cu, or absorb.cu and combine.cu), by its rows and chunks.
+//
+// Above 16 rows, where the mma.sync form leaves its single wave (24 rows: 1.7 us a call less; 96: 4; the
+// kernel alone at 512 rows: 35 and 48).
+inline bool absorb_tc_pays(int rows) { return rows > 16; }
+// One 16-row tile merges faster in clusters of four CTAs a head (launch_combine_mma; a window's call of 8 rows 29 us
+// against 43, of 16 rows 34 and 37).  Above that a cluster takes its rows one pass after another, and this kernel a
+// row's chunks: rows^2 / 6 chunks in all are where the two meet (17 rows of 4.4 chunks 55 us in clusters, 65 here; 20
+// of 3.7: 57 and 62; 24 of 3.1: 65 and 64; 24 of one: 43 and 35; 32: 74 and 64; 40: 91 and 78).
+inline bool project_tc_pays(int rows, long long n_work) { return rows > 16 && 6 * n_work <= (long long)rows * rows; }
+
 // Causal rows: r = (b, j).
 inline int plan_chunk(const int32_t *lens, int batch, int s_q, int units, int granule) {
     return plan_chunk_rows(batch * s_q, [=](int r) { return lens[r / s_q] - s_q + r % s_q + 1; }, units, granule);

@@ -18,8 +18,7 @@ cudaError_t launch_tc_decode(const Dims &d, const void *q_abs, const void *laten
 
 // The per-head products around a view's decode for many rows (head_gemm.cu; bf16, d_nope = d_v = 128,
 // d_c = 512, d_rope = 64): launch_q_absorb_mma and launch_combine_mma (fine) on the 5th-generation tensor cores.
-bool absorb_tc_pays(int rows);
-bool project_tc_pays(int rows, long long n_work);
+// plan_host.h says where they pay.
 cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, const int *seq_lens, int batch, int s_q,
                              void *q_abs, const PlanArgs &plan, cudaStream_t st);
 cudaError_t launch_project_tc(const Dims &d, const float *part_o, const float *part_ml, const int *row_first, int rows,
