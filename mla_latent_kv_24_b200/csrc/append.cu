@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) append_kernel(
     if (n >= n_tok) return;
 
     const int b = req[n], p = pos[n], t = slot[n];   // row t of the request, RoPE at position p
-    if (b < 0 || b >= batch || t < 0 || t >= max_pages * page) {
+    if (b < 0 || b >= batch || t < 0 || t / page >= max_pages) {
         report(err, MLA_ERR_DEVICE_BOUNDS);
         return;
     }
@@ -176,7 +176,7 @@ __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
     float cs = 1.f, sn = 0.f;
     if (stores) {
         int pid = -1;
-        if (req_n >= 0 && req_n < batch && slot_n >= 0 && slot_n < max_pages * 64)
+        if (req_n >= 0 && req_n < batch && slot_n >= 0 && slot_n / 64 < max_pages)
             pid = page_table[(size_t)req_n * max_pages + slot_n / 64];
         if (pid < 0 || pid >= n_pages) report(err, MLA_ERR_DEVICE_BOUNDS);
         else dst = cache + ((size_t)pid * 64 + slot_n % 64) * D_ROW + col;

@@ -37,7 +37,7 @@ __device__ __forceinline__ bool map_row(const RowMap &m, long long i, int page, 
     int p;
     if (m.req) {
         const int b = m.req[i], t = m.pos[i];
-        if (b < 0 || b >= m.batch || t < 0 || t >= m.max_pages * page) {
+        if (b < 0 || b >= m.batch || t < 0 || t / page >= m.max_pages) {
             report(err, MLA_ERR_DEVICE_BOUNDS);
             return false;
         }

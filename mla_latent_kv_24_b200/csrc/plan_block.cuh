@@ -13,13 +13,18 @@
 
 namespace mla {
 
+// The most tokens that a request's page-table row can hold, as far as a length goes.
+__device__ __forceinline__ int plan_max_len(const PlanArgs &a) {
+    return (int)min((long long)a.max_pages * a.page, 0x7fffffffll);
+}
+
 // Tokens of plan row r: a causal row's visible ones, or the window's or tree's virtual length
 // (view.cuh), negative for lengths that cannot be.
 __device__ __forceinline__ int plan_row_len(const PlanArgs &a, int r) {
     const int b = r / a.s_q, j = r % a.s_q, L = a.seq_lens[b];
     if (a.view.kind == VIEW_CAUSAL) return L - a.s_q + j + 1;
     return view_row_len(a.view.kind, a.view.sinks, a.view.window, L, a.view.kind == VIEW_TREE ? a.view.n_nodes[b] : 0,
-                        a.s_q, a.n_q, j, a.page, a.max_pages * a.page);
+                        a.s_q, a.n_q, j, a.page, plan_max_len(a));
 }
 
 // `scratch` is shared memory of the calling block (2 * cap_rows + 1 ints, the block's own
@@ -44,7 +49,7 @@ __device__ __forceinline__ void plan_block(const PlanArgs &a, int *scratch, int 
     for (int r = r0; r < r1; ++r) {
         const int L = a.seq_lens[r / a.s_q];
         const int len = plan_row_len(a, r);
-        if (a.view.kind == VIEW_CAUSAL ? L < a.s_q || L > a.max_pages * a.page : len < 0) atomicOr(&bad, 1);
+        if (a.view.kind == VIEW_CAUSAL ? L < a.s_q || L > plan_max_len(a) : len < 0) atomicOr(&bad, 1);
         if (in_smem) s_len[r] = len;
         local += len > 0 ? ceil_div(len, a.chunk) : 0;
     }
