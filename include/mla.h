@@ -442,8 +442,8 @@ MLA_API mla_status mla_set_profile_events(void *start_event, void *stop_event);
  *   page_table, seq_lens, seq_lens_host as for the decode calls, with n_q <= seq_lens[b].
  *   out           device [batch, n_q, H, d_v].
  *   workspace     >= mla_prefill_workspace_size() bytes, 256-byte aligned (scratch).
- * Needs bf16, d_nope = d_v = 128, d_rope = 64, d_c = 512, page_size = 64
- * (MLA_ERR_UNSUPPORTED otherwise).
+ * Needs bf16, d_nope = d_v = 128, d_rope = 64, d_c = 512, page_size = 64, batch * n_heads <= 65535 and
+ * batch * n_q <= 2^20 (MLA_ERR_UNSUPPORTED otherwise).
  */
 MLA_API mla_status mla_prefill_workspace_size(const mla_dims *dims, int32_t batch, int32_t n_q,
                                               const int32_t *seq_lens_host, size_t *bytes);

@@ -642,6 +642,7 @@ static mla_status prefill_layout(const mla_dims *dims, int32_t batch, int32_t n_
     if (!prefill_ok(*d)) return fail(MLA_ERR_UNSUPPORTED, "prefill needs bf16, d_nope = d_v = 128, d_rope = 64, d_c = 512, page 64");
     if (batch <= 0 || n_q < 1 || !lens) return fail(MLA_ERR_INVALID_ARG, "bad batch / n_q / seq_lens_host");
     if ((long long)batch * n_q > (1 << 20)) return fail(MLA_ERR_UNSUPPORTED, "batch * n_q too large");
+    if ((long long)batch * d->H > 65535) return fail(MLA_ERR_UNSUPPORTED, "batch * n_heads must be <= 65535");   // the kernel's grid
     long long longest = 1;
     for (int b = 0; b < batch; ++b) {
         if (lens[b] < n_q) return fail(MLA_ERR_INVALID_ARG, "seq_lens[%d] = %d < n_q = %d", b, lens[b], n_q);
