@@ -28,11 +28,11 @@
 // lives here, beside the grouped decode whose cache it reads.
 #include <math.h>
 
-#include <cudaTypedefs.h>
 #include <mutex>
 
 #include "tc_decode.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 #include "warp_mma.cuh"
 
 namespace mla {
@@ -64,13 +64,6 @@ constexpr uint64_t WAIT_NS = 2000000000ull;   // 2 s: no legitimate wait comes n
 // 64-column blocks of PAGE rows.
 __device__ __forceinline__ uint32_t sw_off(int r, int c) {
     return (uint32_t)((c >> 6) * BLK + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4));
-}
-__device__ __forceinline__ void tma_load_3d_own(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_own(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -166,8 +159,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
         const int st = i % STAGES;
         const uint32_t full = bars + 8 * st, dst = sbase + STAGE * st;
         tc::mbar_arrive_expect_tx(full, STAGE);
-        tma_load_3d_own(dst, &tm_kv, 0, (pid * G + g) * PAGE, 0, full);
-        tma_load_3d_own(dst + KV_BYTES, &tm_kr, 0, pid * PAGE, 8, full);
+        tc::tma_load_3d(dst, &tm_kv, 0, (pid * G + g) * PAGE, 0, full);
+        tc::tma_load_3d(dst + KV_BYTES, &tm_kr, 0, pid * PAGE, 8, full);
     };
 
     // One tile's query A fragments stay in registers for the whole chunk (12 k-steps of 16 dims);
@@ -441,22 +434,6 @@ static GParams grouped_params(const Dims &d, const void *q, const void *expanded
     return p;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiled g_encode_fn() {
-    static const EncodeTiled fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &qr) == cudaSuccess &&
-            qr == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiled>(ptr);
-        return (EncodeTiled) nullptr;
-    }();
-    return fn;
-}
-
 // The two maps of a (expanded cache, latent cache) pair; a decode loop passes the same buffers
 // every step, so recent encodings are reused (an encoding costs about a microsecond on the host).
 static bool grouped_maps(const void *expanded, const void *latent, int n_pages, int G, CUtensorMap *tm_kv,
@@ -481,20 +458,11 @@ static bool grouped_maps(const void *expanded, const void *latent, int n_pages, 
                 return true;
             }
     }
-    EncodeTiled fn = g_encode_fn();
-    if (!fn) return false;
-    const cuuint32_t estr[3] = {1, 1, 1};
     const cuuint64_t dkv[3] = {64, (cuuint64_t)n_pages * G * PAGE, 4}, skv[2] = {256 * 2, 128};
     const cuuint32_t bkv[3] = {64, PAGE, 4};
     const cuuint64_t dkr[3] = {64, (cuuint64_t)n_pages * PAGE, 9}, skr[2] = {D_ROW * 2, 128};
     const cuuint32_t bkr[3] = {64, PAGE, 1};
-    if (fn(tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(expanded), dkv, skv, bkv, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-        fn(tm_kr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(latent), dkr, skr, bkr, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    if (!encode_bf16_map(tm_kv, expanded, 3, dkv, skv, bkv) || !encode_bf16_map(tm_kr, latent, 3, dkr, skr, bkr)) return false;
     std::lock_guard<std::mutex> lock(mu);
     cache[next] = Entry{expanded, latent, n_pages, G, dev, *tm_kv, *tm_kr};
     next = (next + 1) % 8;

@@ -40,11 +40,11 @@
 // only when a row max grows by more than 2^8 (exact after the final division by l), and only
 // then waits for the previous PV.  Every wait is bounded: on timeout the kernel records
 // MLA_ERR_TIMEOUT, stops issuing work, and still frees its tensor memory before returning.
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include "tc_decode.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace mla {
 namespace {
@@ -691,45 +691,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Looked up once; the initialisation of a function-local static is thread-safe.
-EncodeTiled encode_fn() {
-    static const EncodeTiled fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiled>(ptr);
-        return (EncodeTiled) nullptr;
-    }();
-    return fn;
-}
-
 // Views of a row-major [rows, 576] bf16 matrix whose innermost dimension is one 64-column
 // block (128 bytes, swizzled), so one box gathers several blocks of 64 rows block-major into
 // shared memory.  `nblk` = blocks per box; with `vsplit` the blocks are addressed as
 // [4 blocks per 256-column chunk][2 chunks].  Zero fill past the end.
 bool encode_blocks(CUtensorMap *m, const void *ptr, uint64_t rows, int nblk, bool vsplit) {
-    EncodeTiled fn = encode_fn();
-    if (!fn) return false;
-    cuuint32_t estr[4] = {1, 1, 1, 1};
     if (!vsplit) {
-        cuuint64_t dims[3] = {64, rows, 9};
-        cuuint64_t strides[2] = {DROW * 2, 128};
-        cuuint32_t box[3] = {64, 64, (cuuint32_t)nblk};
-        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        const cuuint64_t dims[3] = {64, rows, 9}, strides[2] = {DROW * 2, 128};
+        const cuuint32_t box[3] = {64, 64, (cuuint32_t)nblk};
+        return encode_bf16_map(m, ptr, 3, dims, strides, box);
     }
-    cuuint64_t dims[4] = {64, rows, 4, 2};
-    cuuint64_t strides[3] = {DROW * 2, 128, 512};
-    cuuint32_t box[4] = {64, 64, 2, 2};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[4] = {64, rows, 4, 2}, strides[3] = {DROW * 2, 128, 512};
+    const cuuint32_t box[4] = {64, 64, 2, 2};
+    return encode_bf16_map(m, ptr, 4, dims, strides, box);
 }
 
 // The maps depend only on (base pointer, rows, box shape); a decode loop passes the same buffers

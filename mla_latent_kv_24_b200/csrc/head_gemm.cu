@@ -13,13 +13,13 @@
 // Every wait is bounded.  A wait that runs out records MLA_ERR_TIMEOUT and ends the CTA's work: nothing more is
 // issued or stored, copies in flight get time to land, and the tensor memory is freed.  The next kernel may launch only once a CTA holds its tensor memory: CTAs of two kernels share an
 // SM's 512 columns, and one that waits for its predecessor must not hold what the predecessor still needs.
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include "plan_block.cuh"
 #include "rope_rows.cuh"
 #include "tc_decode.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 #include "warp_mma.cuh"
 
 namespace mla {
@@ -29,19 +29,6 @@ constexpr int D_C = 512, D_N = 128, D_R = 64, D_QK = 192, D_OUT = 576, D_V = 128
 constexpr int TM = 128;                        // rows of a tile
 constexpr uint32_t BLK = TM * 128;             // 128 rows x 64 bf16, 128-byte swizzled
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
     // At once: until the permit is given up, the SM's other CTAs wait for it with their own allocation.
@@ -118,8 +105,8 @@ __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ 
     bool ok = true;
     if (threadIdx.x == 0) {
         tc::mbar_arrive_expect_tx(full, 6 * BLK);
-        for (int i = 0; i < 2; ++i) tma_load_3d(s.base + AB_A + BLK * i, &tm_q, 64 * i, h, row0, full);
-        for (int i = 0; i < 4; ++i) tma_load_2d(s.base + AB_B + BLK * i, &tm_w, n0 + 64 * i, (h / hpw) * D_N, full);
+        for (int i = 0; i < 2; ++i) tc::tma_load_3d(s.base + AB_A + BLK * i, &tm_q, 64 * i, h, row0, full);
+        for (int i = 0; i < 4; ++i) tc::tma_load_2d(s.base + AB_B + BLK * i, &tm_w, n0 + 64 * i, (h / hpw) * D_N, full);
         ok = tc::mbar_wait_spin(full, 0, wr.limit_ns);
         if (ok) {
             tc::fence_after_sync();
@@ -204,7 +191,7 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
     const int h = blockIdx.x, row0 = blockIdx.y * TM, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     auto load_w = [&](int kb) {
         tc::mbar_arrive_expect_tx(bar(P_FULL + (kb & 1)), BLK);
-        tma_load_2d(s.base + PJ_STAGE * (kb & 1) + 2 * BLK, &tm_w, 64 * kb, (h / hpw) * D_V, bar(P_FULL + (kb & 1)));
+        tc::tma_load_2d(s.base + PJ_STAGE * (kb & 1) + 2 * BLK, &tm_w, 64 * kb, (h / hpw) * D_V, bar(P_FULL + (kb & 1)));
     };
     if (tid == 128) load_w(0), load_w(1);   // streams in while the decode finishes, which has waited for all before the call
     int *k0s = reinterpret_cast<int *>(s.sbase + PJ_INFO), *k1s = k0s + TM;
@@ -381,22 +368,10 @@ __global__ void __launch_bounds__(PJ_THREADS, 1) project_tc_kernel(const __grid_
 // Boxes of 64 columns x 128 rows, 128-byte swizzle: of a row-major matrix [rows, cols], or with heads > 0 of
 // one head of [rows, heads, cols].
 bool encode_box(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t heads) {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &qr) != cudaSuccess ||
-            qr != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    if (!fn) return false;
-    const cuuint32_t estr[3] = {1, 1, 1};
     const cuuint64_t d2[2] = {cols, rows}, s2[1] = {cols * 2};
     const cuuint64_t d3[3] = {cols, heads, rows}, s3[2] = {cols * 2, cols * heads * 2};
     const cuuint32_t b2[2] = {64, TM}, b3[3] = {64, 1, TM};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads ? 3 : 2, const_cast<void *>(ptr), heads ? d3 : d2, heads ? s3 : s2,
-           heads ? b3 : b2, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return heads ? encode_bf16_map(m, ptr, 3, d3, s3, b3) : encode_bf16_map(m, ptr, 2, d2, s2, b2);
 }
 
 }  // namespace

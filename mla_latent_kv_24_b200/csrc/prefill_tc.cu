@@ -23,11 +23,11 @@
 // warp 8 K/Q producer, warp 9 QK^T issuer (leader CTA) and TMEM allocator, warp 10 V producer,
 // warp 11 PV issuer (leader CTA).  Every wait is bounded; a timeout records MLA_ERR_TIMEOUT and the kernel
 // still frees its tensor memory.
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include "tc_decode.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace mla {
 namespace {
@@ -418,34 +418,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Looked up once; the initialisation of a function-local static is thread-safe.
-EncodeTiled pf_encode_fn() {
-    static const EncodeTiled fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &qr) == cudaSuccess &&
-            qr == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiled>(ptr);
-        return (EncodeTiled) nullptr;
-    }();
-    return fn;
-}
-
-// bf16 map with 128-byte swizzle; dims[0] = 64 columns (one block), strides in bytes for dims 1..rank-1.
-bool pf_encode(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-               const cuuint32_t *box) {
-    EncodeTiled fn = pf_encode_fn();
-    if (!fn) return false;
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 cudaError_t launch_prefill_tc(const Dims &d, const void *q_rot, const void *expanded, const void *latent,
@@ -460,20 +432,20 @@ cudaError_t launch_prefill_tc(const Dims &d, const void *q_rot, const void *expa
         const cuuint64_t dims[4] = {64, (cuuint64_t)d.H, (cuuint64_t)plan.rows * n_q, 3};
         const cuuint64_t strides[3] = {D_QK * 2, (cuuint64_t)d.H * D_QK * 2, 128};
         const cuuint32_t box[4] = {64, 1, QT, 3};
-        if (!pf_encode(&tm_q, q_rot, 4, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!encode_bf16_map(&tm_q, q_rot, 4, dims, strides, box)) return cudaErrorInvalidValue;
     }
     {
         const cuuint64_t dims[3] = {64, (cuuint64_t)n_pages * G * PAGE, 4};
         const cuuint64_t strides[2] = {256 * 2, 128};
         const cuuint32_t box_k[3] = {64, PAGE, 2}, box_v[3] = {64, PAGE, 1};
-        if (!pf_encode(&tm_ek, expanded, 3, dims, strides, box_k) || !pf_encode(&tm_ev, expanded, 3, dims, strides, box_v))
+        if (!encode_bf16_map(&tm_ek, expanded, 3, dims, strides, box_k) || !encode_bf16_map(&tm_ev, expanded, 3, dims, strides, box_v))
             return cudaErrorInvalidValue;
     }
     {
         const cuuint64_t dims[3] = {64, (cuuint64_t)n_pages * PAGE, 9};
         const cuuint64_t strides[2] = {576 * 2, 128};
         const cuuint32_t box[3] = {64, PAGE, 1};
-        if (!pf_encode(&tm_kr, latent, 3, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!encode_bf16_map(&tm_kr, latent, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
     PfParams p;
     p.n_q = n_q;
