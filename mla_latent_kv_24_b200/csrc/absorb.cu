@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *q, const int *seq_
         for (int h = 0; h < RH; ++h)
             if (turns && h < nh) {
                 const float x0 = to_f32(x[h].a), x1 = to_f32(x[h].b);
+                // rounds once to the storage type, that of the QK^T operands
                 *reinterpret_cast<Pair *>(dst + (size_t)h * d_qk + d_n + 2 * lane) =
                     Pair{from_f32<T>(x0 * cs - x1 * sn), from_f32<T>(x0 * sn + x1 * cs)};
             }

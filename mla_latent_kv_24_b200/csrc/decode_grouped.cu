@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
                 o[t][n][3] *= a1;
             }
         }
-        // P (accumulator layout of S) is the A fragment of P.V (rows x 16 tokens).
+        // P (accumulator layout of S) is the A fragment of P.V (rows x 16 tokens).  It rounds to bf16, the type of
+        // that product's operands; the row sums above took the unrounded values.
         uint32_t pa[RT][4];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {

@@ -517,6 +517,7 @@ __device__ void run_softmax(const Ctx &c, const TcParams &p, uint32_t tmem, int 
             const float neg_m = VIEW && m_run == -INFINITY ? 0.f : -m_run;
             float sum4[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t pk[16];
+            // P rounds to bf16, the type of the P.V operands; its sum l takes the unrounded values.
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float a = tc::ex2(fmaf(s[2 * j], p.scale_log2, neg_m));

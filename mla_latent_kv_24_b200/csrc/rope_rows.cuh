@@ -53,7 +53,7 @@ __device__ __forceinline__ void rope_or_plan_block(int id, const __nv_bfloat16 *
     float cs, sn;
     rope_cos_sin(query_pos(plan.view, seq_lens, b, j, s_q), theta, &cs, &sn);
     for (int h0 = first; h0 < H; h0 += U * wpr) {
-        uint32_t y[U];
+        uint32_t y[U];   // rounds once to bf16, the type of the QK^T operands, as the absorbed part does
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const float x0 = __uint_as_float(x[i] << 16), x1 = __uint_as_float(x[i] & 0xffff0000u);
