@@ -26,8 +26,8 @@
  *     launch): a kernel may be scheduled while the stream's previous kernel finishes, but it
  *     waits for that kernel's completion before it reads or writes memory, so ordering against
  *     the caller's own work on the stream is that of a plain stream, also behind a kernel that
- *     lets its dependents launch early.  (Before that, weights are at most fetched into L2.)
- *     Stream capture into a CUDA graph records programmatic edges.
+ *     lets its dependents launch early.  Stream capture into a CUDA graph records programmatic
+ *     edges.
  *   - Layouts are row-major and densely packed unless stated.  bf16 = IEEE bfloat16 bits,
  *     fp32 = IEEE float.  All pointers of one call use the dtype in dims->dtype, except int32
  *     index arrays.  Device pointers must be 16-byte aligned.

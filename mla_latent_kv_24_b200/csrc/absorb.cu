@@ -11,8 +11,8 @@
 // rows; every thread owns two latent columns.  The CTAs past the last head are the plan's: the first
 // builds it, which saves a launch (float32 trees of the tiny shape: 23.4 -> 21.3 us a call).
 //
-// Queries, lengths and a tree's arrays may come from the kernel right before the call, so they are read
-// after the wait for it; what W_UK's lines need from HBM is fetched into L2 meanwhile.
+// Queries, lengths and a tree's arrays may come from the kernel right before the call, so the kernels here read
+// nothing before they have waited for it.
 #include "kernels.h"
 #include "plan_block.cuh"
 #include "rope_rows.cuh"
@@ -27,9 +27,6 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *q, const T *W_uk
                                                        int H, int hpw, int d_c, int d_r, int d_n, float base,
                                                        T *__restrict__ q_abs, PlanArgs plan) {
     step_allow_next();
-    if (blockIdx.x < H && grid_tile() == 0 && (int)threadIdx.x < d_n)   // d_c is a multiple of 8
-        prefetch_l2(W_uk + ((size_t)(blockIdx.x / hpw) * d_n + threadIdx.x) * d_c, d_c * (uint32_t)sizeof(T));
-    const double theta = rope_theta(threadIdx.x % (d_r / 2), d_r, base);   // of this thread's first pair
     step_wait_prev();
     __shared__ float qn[RB][128];
     if (blockIdx.x == H) {
@@ -51,8 +48,7 @@ __global__ void __launch_bounds__(256) q_absorb_kernel(const T *q, const T *W_uk
     // RoPE part: pair i of the query's RoPE vector turns by p * base^(-2i/d_r).
     auto angle = [&](int i, float *cs, float *sn) {
         const int row = row0 + i / (d_r / 2);
-        rope_cos_sin(query_pos(plan.view, seq_lens, row / s_q, row % s_q, s_q),
-                     i < (int)blockDim.x ? theta : rope_theta(i % (d_r / 2), d_r, base), cs, sn);
+        rope_cos_sin(query_pos(plan.view, seq_lens, row / s_q, row % s_q, s_q), i % (d_r / 2), d_r, base, cs, sn);
     };
     const int pairs = nr * (d_r / 2);
     float cs = 0.f, sn = 0.f;
@@ -88,9 +84,7 @@ constexpr int RH = 2;
 template <typename T>
 __global__ void __launch_bounds__(256) q_rope_kernel(const T *q, const int *seq_lens, int rows, int s_q, int H,
                                                      int d_r, int d_n, float base, T *__restrict__ q_rot, PlanArgs plan) {
-    step_allow_next();
-    const double theta = rope_theta(threadIdx.x % 32, d_r, base);   // of the lane's pair
-    step_wait_prev();
+    step_begin();
     if (blockIdx.x == gridDim.x - 1) {
         __shared__ int scratch[2 * 512 + 1];
         plan_block<256>(plan, scratch, 512);
@@ -119,7 +113,7 @@ __global__ void __launch_bounds__(256) q_rope_kernel(const T *q, const int *seq_
             if (turns && h < nh) x[h] = *reinterpret_cast<const Pair *>(src + (size_t)h * d_qk + d_n + 2 * lane);
         if (lane < nh * quads) first = *piece(src, lane);
         float cs = 0.f, sn = 0.f;
-        if (turns) rope_cos_sin(p, theta, &cs, &sn);
+        if (turns) rope_cos_sin(p, lane, d_r, base, &cs, &sn);
         if (lane < nh * quads) *piece(dst, lane) = first;
 #pragma unroll 4
         for (int i = lane + 32; i < nh * quads; i += 32) *piece(dst, i) = *piece(src, i);
@@ -175,10 +169,10 @@ cudaError_t launch_q_rope(const Dims &d, const void *q, const int *seq_lens, int
 // for many it is the 147 KB written per row.
 //
 // Two forms.  Up to 16 rows one CTA computes 16 rows x 128 columns of one head, so that a decode step's
-// whole grid (4 column tiles per head) is one wave of CTAs, which waits for the previous kernel together while
-// its W_UK tiles come into L2.  More rows: a CTA keeps its W_UK tile (128 columns) and walks 64-row tiles of the batch, the next tile's queries arriving while this
-// one is multiplied, and stores whole 256-byte row pieces through shared memory.  (With 64 x 64 tiles
-// of their own, 4-byte stores and an angle per head: 82 us for 512 rows, 29 for 128; now 48 and 19.)
+// whole grid (4 column tiles per head) is one wave of CTAs.  More rows: a CTA keeps its W_UK tile (128
+// columns) and walks 64-row tiles of the batch, the next tile's queries arriving while this one is
+// multiplied, and stores whole 256-byte row pieces through shared memory.  (With 64 x 64 tiles of their
+// own, 4-byte stores and an angle per head: 82 us for 512 rows, 29 for 128; now 48 and 19.)
 //
 // The extra columns of blocks build the split plan (their first block) and turn the queries' RoPE part
 // (rope_rows.cuh), so that each pair's double-precision angle is formed once for 16 heads and more.
@@ -222,10 +216,6 @@ __device__ __forceinline__ void absorb_load_w(__nv_bfloat16 *Bs, const __nv_bflo
         cp_async16(Bs + k * AB_LDB + n, Wk + (size_t)k * D_C + n0 + n, true);
     }
 }
-// The same tile into L2, ahead of the wait: one thread a row.
-__device__ __forceinline__ void absorb_prefetch_w(const __nv_bfloat16 *Wk, int n0) {
-    if (threadIdx.x < AB_K) prefetch_l2(Wk + (size_t)threadIdx.x * D_C + n0, AB_N * (uint32_t)sizeof(*Wk));
-}
 template <int TM>
 __device__ __forceinline__ void absorb_load_q(__nv_bfloat16 *As, const __nv_bfloat16 *q, int row0, int rows, int H, int h) {
     for (int c = threadIdx.x; c < TM * AB_K / 8; c += 256) {
@@ -243,10 +233,8 @@ __global__ void __launch_bounds__(256) q_absorb_mma_kernel(const __nv_bfloat16 *
     __shared__ __align__(16) __nv_bfloat16 Bs[AB_K * AB_LDB];       // [128 k][128 n]
     const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
     const __nv_bfloat16 *Wk = W_uk + (size_t)(h / hpw) * D_N * D_C;
-    if (h < H) {
-        absorb_prefetch_w(Wk, n0);
-        step_wait_prev();
-    } else {
+    step_wait_prev();
+    if (h >= H) {
         rope_or_plan_block((h - H) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base, q_abs, plan,
                            reinterpret_cast<int *>(Bs), ((int)sizeof(Bs) / 4 - 1) / 2);
         return;
@@ -285,10 +273,8 @@ __global__ void __launch_bounds__(256, 3) q_absorb_rows_kernel(const __nv_bfloat
     __nv_bfloat16 *As = Bs + AB_K * AB_LDB;                         // [2][64 rows][128 k]; a tile's output too
     const int h = blockIdx.x, n0 = blockIdx.y * AB_N;
     const __nv_bfloat16 *Wk = W_uk + (size_t)(h / hpw) * D_N * D_C;
-    if (h < H) {
-        absorb_prefetch_w(Wk, n0);
-        step_wait_prev();
-    } else {
+    step_wait_prev();
+    if (h >= H) {
         rope_or_plan_block(((h - H) * gridDim.z + blockIdx.z) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base,
                            q_abs, plan, reinterpret_cast<int *>(Bs), (AB_K * AB_LDB / 2 - 1) / 2);
         return;

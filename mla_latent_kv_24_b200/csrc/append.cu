@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256) append_kernel(
         float x0 = acc[2 * half], x1 = acc[2 * half + 1];
         if (c >= d_c) {  // RoPE on the interleaved pair (c - d_c, c - d_c + 1)
             float cs, sn;
-            rope_cos_sin(p, rope_theta((c - d_c) / 2, d_r, base), &cs, &sn);
+            rope_cos_sin(p, (c - d_c) / 2, d_r, base, &cs, &sn);
             float y0 = x0 * cs - x1 * sn, y1 = x0 * sn + x1 * cs;
             x0 = y0;
             x1 = y1;
@@ -153,13 +153,10 @@ __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
         const int col = c0 + r;
         return (col < D_C ? W_dkv + (size_t)col * hidden : W_kr + (size_t)(col - D_C) * hidden) + k0;
     };
-    if (tid < AP_COLS) prefetch_l2(weights(tid), ks * (uint32_t)sizeof(*h));   // ks is a multiple of 32
     // Rank 0's thread stores columns col, col + 1 of token n; its place and angle are found while the tiles arrive.
     static_assert(AP_TOK * AP_COLS / 2 == 256, "a pair of columns per thread");
     const int row = tid / (AP_COLS / 2), n = t0 + row, col = c0 + 2 * (tid % (AP_COLS / 2));
     const bool stores = rank == 0 && n < n_tok;
-    double theta = 0.0;
-    if (stores && col >= D_C) theta = rope_theta((col - D_C) / 2, D_R, base);
     step_wait_prev();   // hidden states and indices may come from the kernel before
     int req_n = -1, pos_n = 0, slot_n = 0;
     if (stores) req_n = req[n], pos_n = pos[n], slot_n = slot[n];
@@ -180,7 +177,7 @@ __global__ void __cluster_dims__(AP_SPLIT, 1, 1) __launch_bounds__(256)
             pid = page_table[(size_t)req_n * max_pages + slot_n / 64];
         if (pid < 0 || pid >= n_pages) report(err, MLA_ERR_DEVICE_BOUNDS);
         else dst = cache + ((size_t)pid * 64 + slot_n % 64) * D_ROW + col;
-        if (col >= D_C) rope_cos_sin(pos_n, theta, &cs, &sn);
+        if (col >= D_C) rope_cos_sin(pos_n, (col - D_C) / 2, D_R, base, &cs, &sn);
     }
     cp_async_wait<0>();
     __syncthreads();

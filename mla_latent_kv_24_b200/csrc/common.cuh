@@ -36,12 +36,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 // RoPE angle for pair i of a d-wide vector at position pos: pos * base^(-2i/d), with the
 // product and the trigonometry in double precision so that large positions (2^17) keep
 // full single-precision accuracy after rounding.
-// In two parts: a pair's frequency does not depend on the position, so kernels form it before they
-// wait for their predecessor.
-__device__ __forceinline__ double rope_theta(int i, int d, float base) {
-    return pow((double)base, -2.0 * (double)i / (double)d);
-}
-__device__ __forceinline__ void rope_cos_sin(int pos, double theta, float *c, float *s) {
+__device__ __forceinline__ void rope_cos_sin(int pos, int i, int d, float base, float *c, float *s) {
+    double theta = pow((double)base, -2.0 * (double)i / (double)d);
     double ang = (double)pos * theta;
     double sd, cd;
     sincos(ang, &sd, &cd);
@@ -63,7 +59,8 @@ __device__ __forceinline__ int grid_tile() { return (int)(blockIdx.z * gridDim.y
 // Programmatic dependent launch.  The kernels of a call are launched with programmatic stream
 // serialisation, so a kernel's CTAs may be launched while the previous kernel of the stream is
 // still running: the caller's own kernel too, when that one lets its dependents launch before its
-// last stores.  So no kernel reads or writes global memory before step_wait_prev(), which waits
+// last stores, and without that as soon as its last block has ended, when its writes need not be visible
+// yet.  So no kernel reads or writes global memory before step_wait_prev(), which waits
 // until the previous kernel has completed and its writes are visible (griddepcontrol.wait).  Every
 // kernel waits in at least one thread of each grid, so a kernel that has completed has seen all its
 // predecessors complete, and execution and memory order stay those of a plain stream.
@@ -73,20 +70,16 @@ __device__ __forceinline__ int grid_tile() { return (int)(blockIdx.z * gridDim.y
 // in a kernel launched without the attribute.  step_begin() is the two in a row, for kernels that do
 // nothing ahead.
 //
-// Two things are done to the caller's memory ahead of the wait.  prefetch_l2() of weights brings
-// lines into L2, where every SM's loads and stores meet, and hands nothing to the kernel.  And the
-// kernels that merge and multiply by W_UV load it: every decode kernel waits before it lets them launch,
-// so that the call's first kernel, and with it all that came before the call, has completed.
+// The one exception: the kernels that merge and multiply by W_UV load it ahead of their wait.  Every
+// decode kernel waits before it lets them launch, so the call's first kernel, and with it all that came
+// before the call, has completed by then.  (Fetching the other kernels' weights into L2 ahead gained nothing
+// measurable, behind other kernels or in a row of calls.)
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ void step_allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void step_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void step_begin() {
     step_wait_prev();
     step_allow_next();
-}
-// `bytes` (a multiple of 16) from the 16-byte aligned `p`.
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
 }
 
 // ---------------------------------------------------------------------------------------

@@ -83,22 +83,19 @@ constexpr uint32_t AB_IDESC = tc::idesc_bf16_f32(TM, 256, false, true);
 
 __global__ void __launch_bounds__(256) absorb_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                         const __grid_constant__ CUtensorMap tm_w,
-                                                        const __nv_bfloat16 *q, const __nv_bfloat16 *W_uk,
-                                                        const int *seq_lens, int rows, int s_q, int H, int hpw,
-                                                        float base, __nv_bfloat16 *__restrict__ q_abs, PlanArgs plan,
-                                                        WaitRule wr) {
+                                                        const __nv_bfloat16 *q, const int *seq_lens, int rows, int s_q,
+                                                        int H, int hpw, float base, __nv_bfloat16 *__restrict__ q_abs,
+                                                        PlanArgs plan, WaitRule wr) {
     extern __shared__ uint8_t hsm[];
     const int h = blockIdx.x, n0 = blockIdx.y * 256, row0 = blockIdx.z * TM;
     if (h >= H) {
-        step_allow_next();
+        step_begin();
         rope_or_plan_block(((h - H) * gridDim.z + blockIdx.z) * gridDim.y + blockIdx.y, q, seq_lens, rows, s_q, H, base,
                            q_abs, plan, reinterpret_cast<int *>(hsm), 4096);
         return;
     }
     const Setup s = set_up<2>(hsm, AB_BAR, 256);
     step_allow_next();
-    if (row0 == 0 && threadIdx.x < D_N)
-        prefetch_l2(W_uk + ((size_t)(h / hpw) * D_N + threadIdx.x) * D_C + n0, 256 * (uint32_t)sizeof(*W_uk));
     step_wait_prev();   // queries may come from the kernel before, and q_abs is workspace that it may still read
     const uint32_t full = s.base + AB_BAR, done = full + 8;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -387,9 +384,8 @@ cudaError_t launch_absorb_tc(const Dims &d, const void *q, const void *W_uk, con
     dim3 grid(d.H + (unsigned)((rope_blocks(rows) + per) / per), 2, z);   // + the plan's and the RoPE blocks
     cudaError_t e = raise_smem_limit((const void *)absorb_tc_kernel, AB_SMEM);
     if (e != cudaSuccess) return e;
-    MLA_STEP_LAUNCH(absorb_tc_kernel, grid, dim3(256), AB_SMEM, st, tm_q, tm_w, (const __nv_bfloat16 *)q,
-                    (const __nv_bfloat16 *)W_uk, seq_lens, rows, s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs, plan,
-                    tc_wait_rule());
+    MLA_STEP_LAUNCH(absorb_tc_kernel, grid, dim3(256), AB_SMEM, st, tm_q, tm_w, (const __nv_bfloat16 *)q, seq_lens, rows,
+                    s_q, d.H, d.hpw, d.base, (__nv_bfloat16 *)q_abs, plan, tc_wait_rule());
     return cudaGetLastError();
 }
 

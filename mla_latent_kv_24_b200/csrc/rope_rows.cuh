@@ -24,12 +24,10 @@ __host__ __device__ __forceinline__ int rope_blocks(int rows) { return ceil_div(
 // A block past the heads' ones, `id` counting them: the first builds the split plan, the next
 // rope_blocks(rows) turn the RoPE part of the queries.  A warp takes every rope_warps()-th head of a row, so
 // that each pair's double-precision angle is formed once for 16 heads and more.  256 threads; `scratch`
-// has 2 cap + 1 ints.  Waits for the previous kernel.
+// has 2 cap + 1 ints.  After step_wait_prev().
 __device__ __forceinline__ void rope_or_plan_block(int id, const __nv_bfloat16 *q, const int *seq_lens, int rows, int s_q,
                                                    int H, float base, __nv_bfloat16 *__restrict__ q_abs,
                                                    const PlanArgs &plan, int *scratch, int cap) {
-    const double theta = rope_theta(threadIdx.x % 32, 64, base);
-    step_wait_prev();
     if (id == 0) {
         plan_block<256>(plan, scratch, cap);
         return;
@@ -51,7 +49,7 @@ __device__ __forceinline__ void rope_or_plan_block(int id, const __nv_bfloat16 *
     };
     load(first);
     float cs, sn;
-    rope_cos_sin(query_pos(plan.view, seq_lens, b, j, s_q), theta, &cs, &sn);
+    rope_cos_sin(query_pos(plan.view, seq_lens, b, j, s_q), lane, 64, base, &cs, &sn);
     for (int h0 = first; h0 < H; h0 += U * wpr) {
         uint32_t y[U];   // rounds once to bf16, the type of the QK^T operands, as the absorbed part does
 #pragma unroll
