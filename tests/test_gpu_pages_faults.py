@@ -150,3 +150,29 @@ def test_a_captured_fork_refused_in_one_replay_and_not_in_the_next():
             p.check()
             p.both("release", (2,))
     del g
+
+
+def test_forks_of_two_pools_on_two_streams():
+    # one pool's forks are carried out while the other's are refused, in no order between them
+    import torch
+    a, b = Pool("dsv2", (100, 0), 8, layers=2, seed=5), Pool("dsv2", (100, 64, 0), 8, layers=2, seed=6)
+    b.lens[2] = -101
+    b.upload()
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    src, dst_a, dst_b = a.i32((0,)), a.i32((1,)), a.i32((2,))
+    torch.cuda.synchronize()
+    for _ in range(200):
+        with torch.cuda.stream(one):
+            mla.mla_cache_fork(a.dims, src, dst_a, 1, *a.tail(), a.d_lat, None, a.layers)
+            mla.mla_cache_release(a.dims, dst_a, None, None, 1, *a.tail())
+        with torch.cuda.stream(two):
+            mla.mla_cache_fork(b.dims, src, dst_b, 1, *b.tail(), b.d_lat, None, b.layers)
+    with torch.cuda.stream(one):
+        mla.mla_cache_fork(a.dims, src, dst_a, 1, *a.tail(), a.d_lat, None, a.layers)
+    torch.cuda.synchronize()
+    refused(5)
+    b.check()
+    # what a released page holds is the last fork's rows: the model makes one fork
+    a.m_fork((0,), (1,))
+    a.check()
